@@ -11,11 +11,14 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
 __all__ = ["chunk_fwd", "chunk_bwd", "chunk_fwd_save", "chunk_bwd_saved", "decode_step",
            "workspace_size", "chunk_path", "get_status",
+           "recurrent_fwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd", "Packed", "pack", "unpack",
+           "chunk_fwd_packed", "chunk_bwd_packed", "Checkpoint", "status_block",
            "lib", "GdnError", "BF16", "F32", "PATH_TCGEN05", "PATH_SIMT"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -28,7 +31,26 @@ LIB_PATH = os.environ.get("GDN_LIBRARY") or os.path.join(_HERE, "libgdn.so")
 BF16, F32 = 0, 1
 PATH_TCGEN05, PATH_SIMT = 1, 2
 
+NORM_NONE, NORM_L2, NORM_RMS = range(3)
+_NORMS = {"none": NORM_NONE, "l2": NORM_L2, "rms": NORM_RMS}
+
 _lib = None
+
+
+class _Rows(ctypes.Structure):          # gdn_rows
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _PackedRows(ctypes.Structure):    # gdn_packed
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class _QkParams(ctypes.Structure):      # gdn_qk_params
+    _fields_ = ([(n, ctypes.c_int32) for n in ("T", "H_q", "H_k", "d", "rot", "interleaved", "norm",
+                                               "dtype")] +
+                [(n, ctypes.c_float) for n in ("eps", "weight_offset", "q_scale", "rope_scale")] +
+                [(n, ctypes.c_void_p) for n in ("positions", "inv_freq", "w_q", "w_k")])
 
 
 class GdnError(RuntimeError):
@@ -91,6 +113,22 @@ def lib() -> ctypes.CDLL:
         L.gdn_chunk_bwd_exact.argtypes = [vp, vp, vp, fp, fp, fp, ip, vp, fp, ci, ci, ci, ci, ci, ci,
                                     ci, fp, fp, fp, fp, fp, fp, vp, sz, vp]
         L.gdn_chunk_bwd_exact.restype = ci
+        i64, rp = ctypes.c_int64, ctypes.POINTER(_Rows)
+        pp, kp = ctypes.POINTER(_QkParams), ctypes.POINTER(_PackedRows)
+        L.gdn_recurrent_fwd.argtypes = ([vp, vp, vp, fp, fp, vp, ip, ip, ip, vp] + [ci] * 6 +
+                                        [i64] * 4 + [ci] * 3 + [vp, vp, vp])
+        L.gdn_recurrent_fwd.restype = ci
+        L.gdn_qk_norm_rope_fwd.argtypes = [pp, rp, rp, rp, rp, kp, kp, vp]
+        L.gdn_qk_norm_rope_fwd.restype = ci
+        L.gdn_qk_norm_rope_fwd_packed.argtypes = [pp, kp, kp, rp, rp, vp]
+        L.gdn_qk_norm_rope_fwd_packed.restype = ci
+        L.gdn_qk_norm_rope_bwd_workspace_size.argtypes = [pp]
+        L.gdn_qk_norm_rope_bwd_workspace_size.restype = sz
+        L.gdn_qk_norm_rope_bwd.argtypes = [pp, rp, rp, ci, rp, rp, rp, rp, fp, fp, vp, sz, vp]
+        L.gdn_qk_norm_rope_bwd.restype = ci
+        L.gdn_qk_norm_rope_bwd_packed.argtypes = [pp, rp, rp, ci, kp, kp, rp, rp, fp, fp, vp, sz,
+                                                  vp]
+        L.gdn_qk_norm_rope_bwd_packed.restype = ci
         L.gdn_get_status.argtypes = [vp, vp]
         L.gdn_get_status.restype = ci
         L.gdn_set_profile_events.argtypes = [vp, vp, vp, vp]
@@ -319,3 +357,297 @@ def _decode_call(fn, name, q, k, v, g, beta, state, out, stream, channel_gate):
             _dtype_code(q.dtype), _stream_ptr(stream))
     _check(rc, name)
     return o
+
+
+# ---------------------------------------------------------------- states of many requests
+
+def status_block(device=None) -> torch.Tensor:
+    """A zeroed control block for the ``status`` argument of ``recurrent_fwd``;
+    hand it to ``get_status`` to read (and clear) what its calls recorded."""
+    return torch.zeros(256, dtype=torch.uint8, device=device or "cuda")
+
+
+def recurrent_fwd(q, k, v, g, beta, pool, slots=None, cu_seqlens=None, keep=None, reset=None,
+                  out=None, status=None, stream=None):
+    """Runs of new tokens of many sequences against a pool of states, which is
+    updated in place. Returns o [T,H_v,d_v].
+
+    q, k: [T,H_k,d_k]; v: [T,H_v,d_v] (bf16 or fp32, one dtype; tokens may be
+    apart, as in slices of a wider projection output); g (= log alpha): [T,H_v],
+    or [T,H_v,d_k] for the channel-wise gate; beta: [T,H_v] (fp32); pool:
+    [num_slots,H_v,d_k,d_v] fp32 or bf16. H_v is a multiple of H_k.
+
+    Run n has tokens cu_seqlens[n] to cu_seqlens[n+1] (int32 [N+1]; without it
+    all N runs have T/N) and its state in slot slots[n] (int32 [N]; without it
+    slot n; negative: padding). The state kept is that after its first keep[n]
+    tokens (int32 [N]; without it all; 0 leaves the slot alone); reset[n] (bool
+    [N]) starts it from zero. Tokens of no run keep what ``out`` held.
+    A run the device finds wrong (see gdn.h) leaves its state alone and has NaN
+    outputs; ``status`` (see ``status_block``) then tells get_status."""
+    dev = _one_device(q, k, v, g, beta, pool, slots, cu_seqlens, keep, reset, out, status)
+    T, Hk, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[2]
+    name = "gdn_recurrent_fwd"
+    _require(name, k.shape == q.shape and v.shape[0] == T, "q, k, v shapes")
+    _require(name, q.dtype == k.dtype == v.dtype, "q, k, v have one dtype")
+    channel = g.dim() == 3
+    _require(name, tuple(g.shape) == ((T, Hv, dk) if channel else (T, Hv)), "shape of g")
+    _require(name, tuple(beta.shape) == (T, Hv), "shape of beta")
+    _require(name, pool.dim() == 4 and tuple(pool.shape[1:]) == (Hv, dk, dv), "shape of pool")
+    _require(name, all(x.dtype == torch.float32 and x.is_contiguous() for x in (g, beta)),
+             "g, beta are contiguous fp32")
+    _require(name, pool.is_contiguous(), "pool is contiguous")
+    N = (cu_seqlens.numel() - 1 if cu_seqlens is not None else
+         slots.numel() if slots is not None else pool.shape[0])
+    for x, t, n in ((slots, torch.int32, N), (cu_seqlens, torch.int32, N + 1),
+                    (keep, torch.int32, N), (reset, torch.bool, N)):
+        _require(name, x is None or (x.dtype == t and x.numel() == n and x.is_contiguous()),
+                 f"an index array is not contiguous {t} of {n}")
+    _require(name, status is None or (status.numel() * status.element_size() >= 256), "status")
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        if out is None:
+            out = torch.empty(T, Hv, dv, dtype=q.dtype, device=dev)
+        _require(name, tuple(out.shape) == (T, Hv, dv) and out.dtype == q.dtype and
+                 out.is_contiguous(), "out")
+        rc = lib().gdn_recurrent_fwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(pool), _ptr(slots),
+            _ptr(cu_seqlens), _ptr(keep), _ptr(reset), N, T, Hk, Hv, dk, dv, pool.shape[0],
+            _token_stride(name, q), _token_stride(name, k), _token_stride(name, v), int(channel),
+            _dtype_code(q.dtype), _dtype_code(pool.dtype), _ptr(out), _ptr(status),
+            _stream_ptr(stream))
+    _check(rc, name)
+    return out
+
+
+def _require(name, ok, what):
+    if not ok:
+        raise ValueError(f"{name}: {what}")
+
+
+def _one_device(*ts):
+    ts = [t for t in ts if t is not None]
+    if not all(t.is_cuda and t.device == ts[0].device for t in ts):
+        raise ValueError("all tensors must be CUDA tensors on one device")
+    return ts[0].device
+
+
+def _token_stride(name, x):
+    """Elements between tokens; heads and channels lie next to each other."""
+    T, H, d = x.shape
+    _require(name, (d <= 1 or x.stride(2) == 1) and (H <= 1 or x.stride(1) == d),
+             "the heads of a token must be contiguous")
+    return x.stride(0) if T > 1 else max(x.stride(0), H * d)
+
+
+# ---------------------------------------------------------------- queries and keys
+
+class Packed(NamedTuple):
+    """Rows in 8 bits: codes [T,H,d] float8_e4m3fn and scales [T,H,ceil(d/32)]
+    uint8; element e stands for codes[e] * 2^(scales[e // 32] - 127)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def _packed_empty(x):
+    T, H, d = x.shape
+    return Packed(torch.empty(T, H, d, dtype=torch.float8_e4m3fn, device=x.device),
+                  torch.empty(T, H, (d + 31) // 32, dtype=torch.uint8, device=x.device))
+
+
+def _packed_arg(name, x):
+    if x is None:
+        return None
+    T, H, d = x[0].shape
+    _require(name, x[0].dtype == torch.float8_e4m3fn and x[1].dtype == torch.uint8 and
+             tuple(x[1].shape) == (T, H, (d + 31) // 32) and x[0].is_contiguous() and
+             x[1].is_contiguous(), "packed rows")
+    return _PackedRows(x[0].data_ptr(), x[1].data_ptr())
+
+
+def _rows_arg(name, x, like=None, dtype=None):
+    if x is None:
+        return None
+    T, H, d = x.shape
+    _require(name, d <= 1 or x.stride(2) == 1, "the channels of a head must be contiguous")
+    _require(name, dtype is None or x.dtype == dtype, f"rows of {x.dtype} for {dtype}")
+    _require(name, like is None or tuple(x.shape) == tuple(like), "shapes of the rows")
+    hs = x.stride(1) if H > 1 else d
+    return _Rows(x.data_ptr(), x.stride(0) if T > 1 else (H - 1) * hs + d, hs)
+
+
+def _qk_params(name, q, k, dtype, w_q, w_k, positions, inv_freq, norm, eps, interleaved,
+               weight_offset, q_scale, rope_scale):
+    T, Hq, d = (q if q is not None else k).shape
+    Hk = 0 if k is None else k.shape[1]
+    _require(name, k is None or (k.shape[0] == T and k.shape[2] == d), "q and k shapes")
+    _require(name, norm in _NORMS, f"norm is one of {sorted(_NORMS)}")
+    _require(name, (positions is None) == (inv_freq is None), "positions come with inv_freq")
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _require(name, rot <= d, "inv_freq has more than d / 2 values")
+        _require(name, inv_freq.dtype == torch.float64 and inv_freq.is_contiguous(),
+                 "inv_freq is contiguous fp64")
+        _require(name, positions.dtype == torch.int32 and positions.is_contiguous() and
+                 positions.numel() == T, "positions are contiguous int32, one a token")
+    for w in (w_q, w_k):
+        _require(name, w is None or (w.dtype == dtype and w.numel() == d and w.is_contiguous()),
+                 "weights are contiguous [d] of the rows' dtype")
+    _require(name, k is not None or w_k is None, "w_k without k")
+    return _QkParams(T, Hq if q is not None else 0, Hk, d, rot, int(interleaved), _NORMS[norm],
+                     _dtype_code(dtype), eps, weight_offset, q_scale, rope_scale,
+                     None if rot == 0 else positions.data_ptr(),
+                     None if rot == 0 else inv_freq.data_ptr(),
+                     None if w_q is None else w_q.data_ptr(),
+                     None if w_k is None else w_k.data_ptr())
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def _is_packed(x):
+    return isinstance(x, tuple)
+
+
+def qk_norm_rope_fwd(q, k, w_q=None, w_k=None, positions=None, inv_freq=None, norm="l2", eps=1e-6,
+                     interleaved=False, weight_offset=0.0, q_scale=1.0, rope_scale=1.0, pack=False,
+                     dtype=None, out=None, stream=None):
+    """Norm of each head's row of q and k and the position rotation, one pass.
+    Returns ``(q_out, k_out)``, with pack=True ``(q_out, k_out, q_packed,
+    k_packed)``: the raw q and k in 8 bits, for the backward pass.
+
+    q: [T,H_q,d], k: [T,H_k,d] or None (bf16 or fp32; tokens and heads may be
+    apart), or both ``Packed`` (then dtype is that of the outputs, bfloat16 if
+    not given). norm: "l2", "rms" or "none"; w_q, w_k: [d] weights (the
+    rows' dtype) or None, to which weight_offset is added; inv_freq: fp64
+    [rot/2] and positions: int32 [T] rotate the first rot elements, by halves
+    or interleaved pairs, times rope_scale; q_scale multiplies q's outputs.
+    out: ``(q_out, k_out)`` to write to; an output may be its own input."""
+    name = "gdn_qk_norm_rope_fwd"
+    packed = _is_packed(q)
+    _require(name, k is None or _is_packed(k) == packed, "q and k both packed, or neither")
+    _require(name, not (packed and pack), "the rows are packed already")
+    qx, kx = (q[0], k and k[0]) if packed else (q, k)
+    extra = (*q, *(k or ())) if packed else (q, k)
+    dev = _one_device(*extra, w_q, w_k, positions, inv_freq, *(out or ()))
+    dtype = (dtype or torch.bfloat16) if packed else qx.dtype
+    p = _qk_params(name, qx, kx, dtype, w_q, w_k, positions, inv_freq, norm, eps, interleaved,
+                   weight_offset, q_scale, rope_scale)
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        if out is None:
+            out = tuple(None if x is None else torch.empty(x.shape, dtype=dtype, device=dev)
+                        for x in (qx, kx))
+        outs = [_rows_arg(name, o, None if x is None else x.shape, dtype)
+                for o, x in zip(out, (qx, kx))]
+        if packed:
+            rc = lib().gdn_qk_norm_rope_fwd_packed(
+                ctypes.byref(p), _ref(_packed_arg(name, q)), _ref(_packed_arg(name, k)),
+                _ref(outs[0]), _ref(outs[1]), _stream_ptr(stream))
+            _check(rc, name + "_packed")
+            return tuple(out)
+        q8, k8 = (None if x is None or not pack else _packed_empty(x) for x in (q, k))
+        rc = lib().gdn_qk_norm_rope_fwd(
+            ctypes.byref(p), _ref(_rows_arg(name, q)), _ref(_rows_arg(name, k, None, dtype)),
+            _ref(outs[0]), _ref(outs[1]), _ref(_packed_arg(name, q8)), _ref(_packed_arg(name, k8)),
+            _stream_ptr(stream))
+    _check(rc, name)
+    return (*out, q8, k8) if pack else tuple(out)
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, w_q=None, w_k=None, positions=None, inv_freq=None,
+                     norm="l2", eps=1e-6, interleaved=False, weight_offset=0.0, q_scale=1.0,
+                     rope_scale=1.0, dtype=None, out=None, workspace=None, stream=None):
+    """Gradients of ``qk_norm_rope_fwd``, whose inputs come again (q, k as they
+    were, or ``Packed``: then at the point the 8-bit rows stand for). dq_out,
+    dk_out: gradients of its outputs (fp32, or the rows' dtype). Returns a dict:
+    dq, dk (the rows' dtype; for packed rows ``dtype``, bfloat16 if not given),
+    dw_q, dw_k ([d] fp32, None without weights). out: ``(dq, dk)`` to write."""
+    name = "gdn_qk_norm_rope_bwd"
+    packed = _is_packed(q)
+    _require(name, k is None or _is_packed(k) == packed, "q and k both packed, or neither")
+    qx, kx = (q[0], k and k[0]) if packed else (q, k)
+    extra = (*q, *(k or ())) if packed else (q, k)
+    dev = _one_device(*extra, dq_out, dk_out, w_q, w_k, positions, inv_freq, *(out or ()))
+    dtype = (dtype or torch.bfloat16) if packed else qx.dtype
+    p = _qk_params(name, qx, kx, dtype, w_q, w_k, positions, inv_freq, norm, eps, interleaved,
+                   weight_offset, q_scale, rope_scale)
+    grads = [_rows_arg(name, g, None if x is None else x.shape, dq_out.dtype)
+             for g, x in zip((dq_out, dk_out), (qx, kx))]
+    _require(name, kx is None or dk_out is not None, "dk_out")
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        if out is None:
+            out = tuple(None if x is None else torch.empty(x.shape, dtype=dtype, device=dev)
+                        for x in (qx, kx))
+        outs = [_rows_arg(name, o, None if x is None else x.shape, dtype)
+                for o, x in zip(out, (qx, kx))]
+        dw = [None if w is None else torch.empty(w.numel(), dtype=torch.float32, device=dev)
+              for w in (w_q, w_k)]
+        need = int(lib().gdn_qk_norm_rope_bwd_workspace_size(ctypes.byref(p)))
+        if need and (workspace is None or workspace.numel() < need):
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        src = ([_packed_arg(name, q), _packed_arg(name, k)] if packed else
+               [_rows_arg(name, q), _rows_arg(name, k, None, dtype)])
+        fn = lib().gdn_qk_norm_rope_bwd_packed if packed else lib().gdn_qk_norm_rope_bwd
+        rc = fn(ctypes.byref(p), _ref(grads[0]), _ref(grads[1]), _dtype_code(dq_out.dtype),
+                _ref(src[0]), _ref(src[1]), _ref(outs[0]), _ref(outs[1]), _ptr(dw[0]), _ptr(dw[1]),
+                _ptr(workspace), need, _stream_ptr(stream))
+    _check(rc, name + ("_packed" if packed else ""))
+    return dict(dq=out[0], dk=out[1], dw_q=dw[0], dw_k=dw[1])
+
+
+def pack(x, stream=None) -> Packed:
+    """Rows [T,H,d] in 8 bits (see ``Packed``)."""
+    return qk_norm_rope_fwd(x, None, norm="none", pack=True, out=(None, None), stream=stream)[2]
+
+
+def unpack(x: Packed, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """The rows that 8-bit rows stand for (exact in bf16 and fp32)."""
+    return qk_norm_rope_fwd(x, None, norm="none", dtype=dtype, stream=stream)[0]
+
+
+# ---------------------------------------------------------------- a training step on 8-bit checkpoints
+
+class Checkpoint(NamedTuple):
+    """What ``chunk_fwd_packed`` keeps for the backward pass: the raw q, k and v
+    in 8 bits (with scales: 3.1 bytes a token, head and channel of d = 128,
+    against 6 for q, k, v in bf16 or 10 with the normed q and k)."""
+    q: Packed
+    k: Packed
+    v: Packed
+    shape: tuple
+    dtype: torch.dtype
+
+
+def chunk_fwd_packed(q, k, v, g, beta, initial_state=None, cu_seqlens=None, chunk=64,
+                     output_final_state=True, stream=None, **norm):
+    """``qk_norm_rope_fwd`` (its keywords in ``norm``; positions [B*T]) and
+    ``chunk_fwd`` of the result, keeping q, k and v in 8 bits for
+    ``chunk_bwd_packed``. q, k, v: [B,T,H,d]. Returns ``(o, final_state or None,
+    Checkpoint)``; o and the state are those of the exact q, k, v."""
+    B, T, H, dk = q.shape
+    dv = v.shape[-1]
+    flat = [x.reshape(B * T, H, x.shape[-1]) for x in (q, k, v)]
+    qn, kn, q8, k8 = qk_norm_rope_fwd(flat[0], flat[1], pack=True, stream=stream, **norm)
+    v8 = pack(flat[2], stream=stream)
+    o, fs = chunk_fwd(qn.view(B, T, H, dk), kn.view(B, T, H, dk), flat[2].view(B, T, H, dv).contiguous(),
+                      g, beta, initial_state, cu_seqlens, chunk, output_final_state, stream=stream)
+    return o, fs, Checkpoint(q8, k8, v8, (B, T, H, dk, dv), q.dtype)
+
+
+def chunk_bwd_packed(ckpt: Checkpoint, g, beta, d_o, initial_state=None, cu_seqlens=None,
+                     d_final_state=None, workspace=None, stream=None, exact=False, **norm):
+    """Gradients of ``chunk_fwd_packed`` from its checkpoint, at the q, k and v
+    that the 8-bit rows stand for. Arguments as there and for ``chunk_bwd``.
+    Returns a dict: dq, dk (of the raw q, k; their dtype), dw_q, dw_k (fp32 or
+    None), dv, dg, dbeta, d_initial_state (fp32)."""
+    B, T, H, dk, dv = ckpt.shape
+    qn, kn = qk_norm_rope_fwd(ckpt.q, ckpt.k, dtype=ckpt.dtype, stream=stream, **norm)
+    v = unpack(ckpt.v, ckpt.dtype, stream=stream)
+    out = chunk_bwd(qn.view(B, T, H, dk), kn.view(B, T, H, dk), v.view(B, T, H, dv), g, beta, d_o,
+                    initial_state, cu_seqlens, d_final_state, workspace, stream, exact)
+    raw = qk_norm_rope_bwd(out["dq"].view(B * T, H, dk), out["dk"].view(B * T, H, dk), ckpt.q, ckpt.k,
+                           dtype=ckpt.dtype, stream=stream, **norm)
+    out.update(dq=raw["dq"].view(B, T, H, dk), dk=raw["dk"].view(B, T, H, dk), dw_q=raw["dw_q"],
+               dw_k=raw["dw_k"])
+    return out

@@ -17,7 +17,8 @@
  *     allocates no memory and frees none.
  *   - Calls are asynchronous on `stream` (a cudaStream_t passed as void*;
  *     NULL = the legacy default stream) and return once work is enqueued.
- *   - Inputs are never modified, except `state` in gdn_decode_step.
+ *   - Inputs are never modified, except `state` in gdn_decode_step and `pool` in
+ *     gdn_recurrent_fwd.
  *   - Outputs are undefined when a call returns an error.
  *   - Row-major layouts:
  *       q, k   [B, T, H, d_k]      v, o   [B, T, H, d_v]
@@ -387,6 +388,144 @@ int gdn_chunk_bwd_exact(const void *q, const void *k, const void *v, const float
                         float *dq, float *dk, float *dv, float *dg, float *dbeta,
                         float *d_initial_state, void *workspace, size_t workspace_bytes,
                         void *stream);
+
+/*
+ * gdn_recurrent_fwd -- the recurrence above for runs of new tokens of many
+ * sequences against a pool of states, updated in place: the decode step of a
+ * server, the check of drafted tokens, short prompts. (The pages' "constant
+ * size state, no KV cache", phantomic12 page, mechanism paragraph, with the
+ * states of all requests in one allocation.) Unlike gdn_decode_step, a run has
+ * any number of tokens, its state is found by slot and may be bf16, and several
+ * value heads may share a query/key head.
+ *
+ *   q, k       [T, H_k, d_k] (dtype): token t's heads start at t * q_stride
+ *              (k_stride) elements and lie next to each other, so slices of a
+ *              wider projection output can be passed as they are.
+ *   v          [T, H_v, d_v] likewise, v_stride; H_v a multiple of H_k, value
+ *              head h reads query/key head h / (H_v / H_k).
+ *   g          [T, H_v] fp32, or [T, H_v, d_k] with channel_gate != 0 (the
+ *              channel-wise gate below); beta [T, H_v] fp32. Both contiguous.
+ *   pool       [num_slots, H_v, d_k, d_v] of state_dtype (S^T, as `state`),
+ *              16-byte aligned. All arithmetic is fp32; a bf16 pool rounds the
+ *              state once a call, when it is stored.
+ *   slots      int32 [N] or NULL (run n uses slot n): where run n's state lies.
+ *              Negative: run n is padding, nothing of it is read or written.
+ *   cu_seqlens int32 [N + 1] or NULL: run n covers tokens [cu[n], cu[n+1])
+ *              (empty runs allowed); tokens outside every run are left alone.
+ *              NULL: T / N tokens a run, T a multiple of N.
+ *   keep       int32 [N] or NULL (all): the stored state is that after the
+ *              run's first keep[n] tokens (0: the slot is left as it was); the
+ *              outputs are those of the whole run. Drafted tokens are checked
+ *              by running them after the accepted ones with keep at the latter.
+ *   reset      bytes [N] or NULL: non-zero starts run n from a zero state
+ *              instead of what its slot holds.
+ *   o          [T, H_v, d_v] (dtype), contiguous, aligned to four elements.
+ *   status     NULL, or a 256-byte control block, zeroed by the caller before
+ *              its first use, for gdn_get_status(status, stream).
+ * A slot that two runs name, when either stores its state, a slot outside the
+ * pool, a keep outside [0, length] and tokens outside [0, T] are found on the
+ * device: that run's state is left alone, its outputs (unless its tokens are
+ * the bad part) are NaN, and the status is GDN_ERR_INVALID_ARG. Runs that keep
+ * nothing may share a slot. d_k, d_v <= 128, d_v a multiple of 4. No workspace;
+ * the call can be captured, and calls on disjoint slots may overlap.
+ */
+int gdn_recurrent_fwd(const void *q, const void *k, const void *v, const float *g,
+                      const float *beta, void *pool, const int32_t *slots,
+                      const int32_t *cu_seqlens, const int32_t *keep, const uint8_t *reset, int N,
+                      int T, int H_k, int H_v, int d_k, int d_v, int64_t num_slots,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride, int channel_gate,
+                      int dtype, int state_dtype, void *o, void *status, void *stream);
+
+/*
+ * Norms of queries and keys, with the position rotation in the same pass. The
+ * recurrence wants unit keys (the pages' transition I - beta k k^T contracts
+ * for |k| = 1); these entry points make q and k for the calls above from a
+ * projection's output, and take the gradients back through it. Per row x of d
+ * elements (token t, one head):
+ *
+ *     r = (sum x^2 + eps)^-1/2  (GDN_NORM_L2),  (mean x^2 + eps)^-1/2
+ *         (GDN_NORM_RMS),  1 (GDN_NORM_NONE)
+ *     z = (w + weight_offset) x r           (w per channel, or NULL: z = x r)
+ *     y = [ rope_scale R z[0:rot] , z[rot:d] ],  q's times q_scale
+ *
+ * R turns the pairs (j, j + rot/2), or (2j, 2j + 1) when interleaved, by
+ * positions[t] * inv_freq[j], j < rot/2. The frequencies are fp64 and the
+ * caller's, so any stretching for long contexts is theirs to choose, and the
+ * angle is reduced in fp64, so far positions are exact to fp32.
+ */
+#define GDN_NORM_NONE 0
+#define GDN_NORM_L2   1
+#define GDN_NORM_RMS  2
+
+/* Rows of T tokens' heads in device memory, strides in elements: element e of
+ * head h of token t at data[t * token_stride + h * head_stride + e]. Aligned to
+ * its element size; whole 16-byte rows are read fastest. */
+typedef struct {
+  void *data;
+  int64_t token_stride, head_stride;
+} gdn_rows;
+
+/* Rows in 8 bits: codes [T, H, d] in e4m3 and scales [T, H, ceil(d / 32)], both
+ * contiguous. Element e stands for codes[e] * 2^(scales[e / 32] - 127). The
+ * scale is the smallest power of two (down to 2^-127) that takes the block's
+ * largest finite magnitude to 448 or less; codes are rounded to nearest even;
+ * what is not finite becomes NaN. Exact in bf16 and fp32, but that magnitudes
+ * from 1.9375 * 2^127 up are rounded to 2^128, an infinity there. */
+typedef struct {
+  uint8_t *codes, *scales;
+} gdn_packed;
+
+typedef struct {
+  int32_t T, H_q, H_k, d;          /* tokens; heads of q and of k (0: absent); d <= 256 */
+  int32_t rot;                     /* elements of a head that turn: even, 0 .. d */
+  int32_t interleaved;             /* which pairs turn together */
+  int32_t norm;                    /* GDN_NORM_* */
+  int32_t dtype;                   /* of the rows and of w_q, w_k */
+  float eps, weight_offset, q_scale, rope_scale;
+  const int32_t *positions;        /* [T]; NULL when rot = 0 */
+  const double *inv_freq;          /* [rot / 2]; NULL when rot = 0 */
+  const void *w_q, *w_k;           /* [d] or NULL */
+} gdn_qk_params;
+
+/*
+ * gdn_qk_norm_rope_fwd -- q_out, k_out from q, k. With q_packed (k_packed) not
+ * NULL the raw q (k) is also written in 8 bits, for the backward pass; then
+ * q_out (k_out) may be NULL, or have NULL data, to write the codes alone. An
+ * output may be its own input (same data and strides), otherwise they must not
+ * overlap. No workspace.
+ */
+int gdn_qk_norm_rope_fwd(const gdn_qk_params *p, const gdn_rows *q, const gdn_rows *k,
+                         const gdn_rows *q_out, const gdn_rows *k_out, const gdn_packed *q_packed,
+                         const gdn_packed *k_packed, void *stream);
+
+/* gdn_qk_norm_rope_fwd_packed -- the same outputs (dtype) from rows in 8 bits:
+ * the operands of gdn_chunk_bwd again, from the checkpoint. */
+int gdn_qk_norm_rope_fwd_packed(const gdn_qk_params *p, const gdn_packed *q, const gdn_packed *k,
+                                const gdn_rows *q_out, const gdn_rows *k_out, void *stream);
+
+/* Bytes of workspace the two backward entry points need on the current device:
+ * 0 without weights. */
+size_t gdn_qk_norm_rope_bwd_workspace_size(const gdn_qk_params *p);
+
+/*
+ * gdn_qk_norm_rope_bwd -- gradients dq, dk (dtype) of the raw rows, and dw_q,
+ * dw_k ([d] fp32, wanted exactly when w_q, w_k are given) for gradients dq_out,
+ * dk_out of the outputs, which have grad_dtype (GDN_F32, as gdn_chunk_bwd
+ * leaves them, or dtype). The weights' gradients are summed in a fixed order.
+ * workspace: 256-byte aligned, not shared with a concurrent call.
+ */
+int gdn_qk_norm_rope_bwd(const gdn_qk_params *p, const gdn_rows *dq_out, const gdn_rows *dk_out,
+                         int grad_dtype, const gdn_rows *q, const gdn_rows *k, const gdn_rows *dq,
+                         const gdn_rows *dk, float *dw_q, float *dw_k, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* gdn_qk_norm_rope_bwd_packed -- the same gradients at the point that the 8-bit
+ * rows stand for: the norm is formed again from them. */
+int gdn_qk_norm_rope_bwd_packed(const gdn_qk_params *p, const gdn_rows *dq_out,
+                                const gdn_rows *dk_out, int grad_dtype, const gdn_packed *q,
+                                const gdn_packed *k, const gdn_rows *dq, const gdn_rows *dk,
+                                float *dw_q, float *dw_k, void *workspace, size_t workspace_bytes,
+                                void *stream);
 
 /*
  * gdn_selftest_wait_timeout -- device self-test of the bounded waits (the

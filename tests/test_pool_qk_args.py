@@ -1,0 +1,160 @@
+"""Host-side refusals of the pooled recurrent rule and of the query/key norms: found before anything is
+launched, so no GPU is needed; and the formulas' gradients against differences in fp64."""
+import ctypes
+
+import pytest
+import torch
+
+import gated_delta_rule_112_b200 as gdn
+from gated_delta_rule_112_b200 import build as gbuild
+
+P = ctypes.c_void_p(1 << 20)
+ODD = ctypes.c_void_p((1 << 20) + 2)
+
+
+@pytest.fixture(scope="module")
+def L():
+    gbuild.build()
+    return gdn.lib()
+
+
+def recurrent(L, **kw):
+    a = dict(q=P, k=P, v=P, g=P, beta=P, pool=P, slots=P, cu=P, keep=None, reset=None, N=2, T=4, Hk=2, Hv=4,
+             dk=128, dv=128, P=8, qs=256, ks=256, vs=512, channel=0, dtype=gdn.BF16, sdt=gdn.F32, o=P,
+             status=None)
+    a.update(kw)
+    return L.gdn_recurrent_fwd(a["q"], a["k"], a["v"], a["g"], a["beta"], a["pool"], a["slots"], a["cu"],
+                               a["keep"], a["reset"], a["N"], a["T"], a["Hk"], a["Hv"], a["dk"], a["dv"],
+                               a["P"], a["qs"], a["ks"], a["vs"], a["channel"], a["dtype"], a["sdt"], a["o"],
+                               a["status"], None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dtype=5), dict(sdt=2), dict(Hk=3), dict(Hk=0), dict(N=-1), dict(T=-1), dict(dk=0), dict(dv=0),
+    dict(P=-1), dict(cu=None, N=3), dict(slots=None, N=9), dict(qs=255), dict(ks=8), dict(vs=511),
+    dict(q=None), dict(k=None), dict(v=None), dict(g=None), dict(beta=None), dict(pool=None), dict(o=None),
+    dict(pool=ODD), dict(o=ODD), dict(g=ODD), dict(beta=ODD), dict(slots=ODD), dict(cu=ODD), dict(keep=ODD),
+    dict(status=ODD), dict(q=ctypes.c_void_p((1 << 20) + 1)),
+])
+def test_recurrent_refuses(L, bad):
+    assert recurrent(L, **bad) == gdn.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", [dict(dk=129, qs=512, ks=512), dict(dv=132, vs=600), dict(dv=126),
+                                 dict(N=1 << 29)])
+def test_recurrent_unsupported(L, bad):
+    assert recurrent(L, **bad) == gdn.ERR_UNSUPPORTED
+
+
+def test_recurrent_without_work(L):
+    assert recurrent(L, N=0, T=0, slots=None) == gdn.OK
+    assert recurrent(L, T=0) == gdn.OK
+
+
+def rows(p=1 << 20, ts=1 << 16, hs=128):
+    return gdn._Rows(p, ts, hs)
+
+
+def params(**kw):
+    a = dict(T=4, H_q=2, H_k=2, d=128, rot=64, interleaved=0, norm=gdn.NORM_L2, dtype=gdn.BF16, eps=1e-6,
+             weight_offset=0.0, q_scale=1.0, rope_scale=1.0, positions=1 << 20, inv_freq=1 << 20, w_q=None,
+             w_k=None)
+    a.update(kw)
+    return gdn._QkParams(**a)
+
+
+BAD_PARAMS = [dict(dtype=3), dict(T=-1), dict(H_q=-1), dict(H_k=-1), dict(d=0), dict(rot=63), dict(rot=-2),
+              dict(rot=130), dict(norm=3), dict(norm=-1), dict(positions=None), dict(inv_freq=None),
+              dict(positions=(1 << 20) + 2), dict(inv_freq=(1 << 20) + 4), dict(w_q=(1 << 20) + 1)]
+
+
+@pytest.mark.parametrize("bad", BAD_PARAMS)
+def test_norm_refuses_parameters(L, bad):
+    p, r, k8 = params(**bad), ctypes.byref(rows()), ctypes.byref(gdn._PackedRows(1 << 20, 1 << 20))
+    pp = ctypes.byref(p)
+    assert L.gdn_qk_norm_rope_fwd(pp, r, r, r, r, None, None, None) == gdn.ERR_INVALID_ARG
+    assert L.gdn_qk_norm_rope_fwd_packed(pp, k8, k8, r, r, None) == gdn.ERR_INVALID_ARG
+    assert L.gdn_qk_norm_rope_bwd(pp, r, r, gdn.F32, r, r, r, r, P, P, P, 1 << 30, None) == gdn.ERR_INVALID_ARG
+    assert L.gdn_qk_norm_rope_bwd_packed(pp, r, r, gdn.F32, k8, k8, r, r, P, P, P, 1 << 30,
+                                         None) == gdn.ERR_INVALID_ARG
+
+
+def test_norm_refuses_rows(L):
+    good, p = ctypes.byref(rows()), ctypes.byref(params())
+    k8 = ctypes.byref(gdn._PackedRows(1 << 20, 1 << 20))
+    for bad in (rows(None), rows((1 << 20) + 1), rows(hs=127), rows(ts=255)):
+        b = ctypes.byref(bad)
+        assert L.gdn_qk_norm_rope_fwd(p, b, good, good, good, None, None, None) == gdn.ERR_INVALID_ARG
+        assert L.gdn_qk_norm_rope_fwd(p, good, good, good, b, None, None, None) == gdn.ERR_INVALID_ARG
+        assert L.gdn_qk_norm_rope_bwd(p, b, good, gdn.F32, good, good, good, good, None, None, None, 0,
+                                      None) == gdn.ERR_INVALID_ARG
+        assert L.gdn_qk_norm_rope_bwd(p, good, good, gdn.F32, good, good, good, b, None, None, None, 0,
+                                      None) == gdn.ERR_INVALID_ARG
+    assert L.gdn_qk_norm_rope_fwd(p, None, good, good, good, None, None, None) == gdn.ERR_INVALID_ARG
+    assert L.gdn_qk_norm_rope_fwd(p, good, good, None, good, None, None, None) == gdn.ERR_INVALID_ARG
+    for bad8 in (gdn._PackedRows(None, 1 << 20), gdn._PackedRows(1 << 20, None)):
+        assert L.gdn_qk_norm_rope_fwd_packed(p, ctypes.byref(bad8), k8, good, good, None) == gdn.ERR_INVALID_ARG
+    assert L.gdn_qk_norm_rope_fwd(p, good, good, good, good,
+                                  ctypes.byref(gdn._PackedRows(1 << 20, None)), None, None) == gdn.ERR_INVALID_ARG
+
+
+def test_norm_unsupported_and_workspace(L):
+    r = ctypes.byref(rows(hs=300))
+    assert L.gdn_qk_norm_rope_fwd(ctypes.byref(params(d=257)), r, r, r, r, None, None, None) == gdn.ERR_UNSUPPORTED
+    f = ctypes.byref(params(dtype=gdn.F32))
+    assert L.gdn_qk_norm_rope_bwd(f, r, r, gdn.BF16, r, r, r, r, None, None, None, 0, None) == gdn.ERR_UNSUPPORTED
+    p = ctypes.byref(params())
+    assert L.gdn_qk_norm_rope_bwd(p, r, r, 7, r, r, r, r, None, None, None, 0, None) == gdn.ERR_INVALID_ARG
+    # weights and their gradients come together, with a workspace
+    assert L.gdn_qk_norm_rope_bwd(p, r, r, gdn.F32, r, r, r, r, P, None, P, 1 << 30, None) == gdn.ERR_INVALID_ARG
+    w = ctypes.byref(params(w_q=1 << 20))
+    assert L.gdn_qk_norm_rope_bwd(w, r, r, gdn.F32, r, r, r, r, None, None, P, 1 << 30, None) == gdn.ERR_INVALID_ARG
+    assert L.gdn_qk_norm_rope_bwd(w, r, r, gdn.F32, r, r, r, r, P, None, None, 1 << 30, None) == gdn.ERR_WORKSPACE
+    assert L.gdn_qk_norm_rope_bwd_workspace_size(p) == 0
+
+
+def test_norm_without_work(L):
+    p, r = ctypes.byref(params(T=0, positions=None, inv_freq=None)), ctypes.byref(rows())
+    assert L.gdn_qk_norm_rope_fwd(p, r, r, r, r, None, None, None) == gdn.OK
+    assert L.gdn_qk_norm_rope_fwd(p, None, None, None, None, None, None, None) == gdn.OK
+
+
+def test_binding_refuses_cpu_tensors():
+    x = torch.zeros(2, 2, 128)
+    with pytest.raises(ValueError):
+        gdn.qk_norm_rope_fwd(x, x)
+    with pytest.raises(ValueError):
+        gdn.recurrent_fwd(x, x, x, x[..., 0], x[..., 0], torch.zeros(2, 2, 128, 128))
+
+
+@pytest.mark.parametrize("norm", ["l2", "rms", "none"])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_formula_gradients_against_differences(norm, interleaved):
+    """dx = r (dh - h (dh . h) / n) and dw, with the rotation undone, against central differences, fp64:
+    step 1e-5, so h^2 and 1e-16 / h both stay below 1e-9 of the gradient's scale."""
+    from tests.test_qk_norm_gpu import inv_freq, plain
+    gen = torch.Generator().manual_seed(5)
+    T, H, d, rot, eps = 2, 2, 12, 8, 1e-2
+    x = torch.randn(T, H, d, generator=gen, dtype=torch.float64)
+    w = torch.randn(d, generator=gen, dtype=torch.float64)
+    dy = torch.randn(T, H, d, generator=gen, dtype=torch.float64)
+    how = dict(norm=norm, eps=eps, interleaved=interleaved, inv_freq=inv_freq(rot), rope_scale=1.2,
+               positions=torch.tensor([3, 77], dtype=torch.int32))
+    back = dict(norm="none", interleaved=interleaved, inv_freq=inv_freq(rot), rope_scale=1.2,
+                positions=-how["positions"])
+    n = d if norm == "rms" else 1
+    r = torch.ones(T, H, 1, dtype=torch.float64) if norm == "none" else \
+        ((x * x).sum(-1, keepdim=True) / n + eps).rsqrt()
+    h, dz = x * r, plain(dy, None, back)
+    dw, dh = (dz * h).sum((0, 1)), dz * w
+    dx = dh if norm == "none" else r * (dh - h * (dh * h).sum(-1, keepdim=True) / n)
+    for a, grad in ((x, dx), (w, dw)):
+        num, flat = torch.zeros_like(a), a.view(-1)
+        for i in range(flat.numel()):
+            old, vals = float(flat[i]), []
+            for step in (1e-5, -1e-5):
+                flat[i] = old + step
+                vals.append(float((plain(x, w, how) * dy).sum()))
+            flat[i] = old
+            num.view(-1)[i] = (vals[0] - vals[1]) / 2e-5
+        assert float((num - grad).norm() / grad.norm()) < 1e-8

@@ -1,0 +1,325 @@
+"""gdn_recurrent_fwd against the fp64 oracle's token recurrence, run by run.
+
+Tolerances (relative L2): fp32 results TOL_F32; results stored in bf16 also get
+half a bf16 step, 2^-8 of each value, which bounds the relative L2 of rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from tests.parity import TOL_F32, assert_close, np64
+
+pytestmark = pytest.mark.gpu
+
+
+def tol(dtype):
+    return TOL_F32 + (torch.finfo(dtype).eps / 2 if dtype == torch.bfloat16 else 0.0)
+
+
+def make(lens, Hk, Hv, dk, dv, dtype=torch.bfloat16, pool_dtype=torch.float32, channel=False,
+         spare=3, seed=0, gmean=-2.0, beta_scale=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    T, N = sum(lens), len(lens)
+    q, k = (torch.nn.functional.normalize(torch.randn(T, Hk, dk, generator=gen), dim=-1).to(dtype)
+            for _ in "qk")
+    d = dict(q=q, k=k, v=torch.randn(T, Hv, dv, generator=gen).to(dtype),
+             g=-torch.nn.functional.softplus(
+                 torch.randn((T, Hv, dk) if channel else (T, Hv), generator=gen) + gmean),
+             beta=beta_scale * torch.sigmoid(torch.randn(T, Hv, generator=gen)),
+             pool=(0.3 * torch.randn(N + spare, Hv, dk, dv, generator=gen)).to(pool_dtype),
+             slots=torch.randperm(N + spare, generator=gen)[:N].to(torch.int32),
+             cu=torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32))
+    d["lens"] = list(lens)
+    return d
+
+
+def reference(d, keep=None, reset=None, slots=None):
+    """o [T,Hv,dv] and the pool after the call, fp64, from the oracle run by run."""
+    lens = d["lens"]
+    q, k, v, g, b, pool = (np64(d[x]) for x in ("q", "k", "v", "g", "beta", "pool"))
+    rep = v.shape[1] // q.shape[1]
+    q, k = q.repeat(rep, 1), k.repeat(rep, 1)
+    fn = oracle.kda_chunk_fwd if g.ndim == 3 else oracle.chunk_fwd
+    o = np.zeros_like(v)
+    at = 0
+    slots = d["slots"].tolist() if slots is None else slots
+    out = pool.copy()
+    for n, length in enumerate(lens):
+        rows = slice(at, at + length)
+        at += length
+        if length == 0 or slots[n] < 0:
+            continue
+        s0 = pool[slots[n]][None]
+        if reset is not None and reset[n]:
+            s0 = np.zeros_like(s0)
+        m = length if keep is None else keep[n]
+        o[rows] = fn(q[rows][None], k[rows][None], v[rows][None], g[rows][None], b[rows][None],
+                     s0)[0][0]
+        if m:
+            r = slice(rows.start, rows.start + m)
+            out[slots[n]] = fn(q[r][None], k[r][None], v[r][None], g[r][None], b[r][None], s0)[1][0]
+    return o, out
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def call(d, keep=None, reset=None, slots=None, cu=True, out=None, status=None, stream=None):
+    import gated_delta_rule_112_b200 as gdn
+    pool = d["pool"].cuda()
+    o = gdn.recurrent_fwd(
+        *(d[x].cuda() for x in ("q", "k", "v", "g", "beta")), pool,
+        slots=d["slots"].cuda() if slots is None else ints(slots),
+        cu_seqlens=d["cu"].cuda() if cu else None, keep=None if keep is None else ints(keep),
+        reset=None if reset is None else torch.tensor(reset, dtype=torch.bool, device="cuda"),
+        out=out, status=status, stream=stream)
+    return o, pool
+
+
+def check(d, o, pool, **how):
+    ro, rp = reference(d, **how)
+    if ro.size:
+        assert_close("o", np64(o), ro, tol(d["v"].dtype))
+    assert_close("pool", np64(pool), rp, tol(pool.dtype))
+
+
+BF, F = torch.bfloat16, torch.float32
+CASES = [
+    # lens, Hk, Hv, dk, dv, dtype, pool dtype, channel gate
+    ([1], 1, 1, 128, 128, BF, F, False),
+    ([1] * 7, 2, 2, 128, 128, BF, F, False),
+    ([1] * 5, 2, 6, 128, 128, F, F, True),
+    ([3, 1, 0, 6, 2], 4, 4, 128, 128, BF, F, False),
+    ([9, 8, 7, 17], 1, 4, 128, 128, BF, BF, False),
+    ([5, 0, 33], 3, 3, 96, 80, F, F, False),
+    ([2, 70], 2, 4, 64, 128, BF, F, True),
+    ([4, 5], 1, 2, 36, 20, F, BF, True),
+    ([6], 5, 5, 128, 4, F, F, False),
+    ([1, 2, 3], 2, 2, 1, 8, F, F, False),
+    ([11, 3], 1, 3, 33, 12, BF, F, True),
+    ([300, 129], 1, 1, 128, 64, F, F, False),
+]
+
+
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_runs_match_oracle(case):
+    lens, Hk, Hv, dk, dv, dtype, pdt, channel = CASES[case]
+    d = make(lens, Hk, Hv, dk, dv, dtype, pdt, channel, seed=case)
+    o, pool = call(d)
+    check(d, o, pool)
+    others = sorted(set(range(d["pool"].shape[0])) - set(d["slots"].tolist()))
+    assert torch.equal(pool[others].cpu(), d["pool"][others])       # slots of nobody: untouched
+
+
+@pytest.mark.parametrize("channel", [False, True])
+@pytest.mark.parametrize("pdt", [F, BF])
+def test_keep_and_reset(channel, pdt):
+    lens = [6, 6, 6, 1, 12, 0]
+    keep, reset = [0, 3, 6, 0, 9, 0], [False, True, False, True, True, True]
+    d = make(lens, 2, 4, 128, 128, BF, pdt, channel, seed=20)
+    o, pool = call(d, keep=keep, reset=reset)
+    check(d, o, pool, keep=keep, reset=reset)
+    for n in (0, 3, 5):                                             # nothing kept: bit for bit
+        s = d["slots"][n]
+        assert torch.equal(pool[s].cpu(), d["pool"][s])
+
+
+def test_equal_lengths_without_cu_and_without_slots():
+    import gated_delta_rule_112_b200 as gdn
+    d = make([4] * 3, 2, 2, 128, 128, F, seed=21, spare=0)
+    d["slots"] = torch.arange(3, dtype=torch.int32)
+    pool = d["pool"].cuda()
+    o = gdn.recurrent_fwd(*(d[x].cuda() for x in ("q", "k", "v", "g", "beta")), pool)
+    check(d, o, pool)
+
+
+def test_matches_decode_step():
+    import gated_delta_rule_112_b200 as gdn
+    for channel in (False, True):
+        d = make([1] * 6, 3, 3, 128, 128, F, seed=22, channel=channel, spare=0)
+        d["slots"] = torch.arange(6, dtype=torch.int32)
+        o, pool = call(d)
+        state = d["pool"].cuda()
+        step = gdn.kda_decode_step if channel else gdn.decode_step
+        ref = step(*(d[x].cuda() for x in ("q", "k", "v", "g", "beta")), state)
+        assert_close("o", np64(o), np64(ref), TOL_F32)
+        assert_close("state", np64(pool), np64(state), TOL_F32)
+
+
+def test_one_call_equals_two():
+    d = make([13, 9], 1, 2, 128, 128, F, seed=23)
+    o, pool = call(d)
+    import gated_delta_rule_112_b200 as gdn
+    p2 = d["pool"].cuda()
+    parts = []
+    for (a0, b0), (a1, b1) in (((0, 5), (13, 17)), ((5, 13), (17, 22))):   # tokens of each run, call by call
+        rows = torch.cat([torch.arange(a0, b0), torch.arange(a1, b1)])
+        parts.append((rows, gdn.recurrent_fwd(
+            *(d[x][rows].cuda() for x in ("q", "k", "v", "g", "beta")), p2, d["slots"].cuda(),
+            ints([0, b0 - a0, len(rows)]))))
+    both = torch.empty_like(o)
+    for rows, y in parts:
+        both[rows.cuda()] = y
+    assert_close("o", np64(both), np64(o), TOL_F32)
+    assert_close("pool", np64(p2), np64(pool), TOL_F32)
+
+
+def test_padding_and_tokens_behind_the_last_run_are_left_alone():
+    d = make([2, 3, 1], 2, 2, 128, 128, BF, seed=24)
+    slots = [int(d["slots"][0]), -1, int(d["slots"][2])]
+    extra = 5                                                      # padded rows of a captured batch
+    for x in ("q", "k", "v", "g", "beta"):
+        d[x] = torch.cat([d[x], torch.full_like(d[x][:1], float("nan")).expand(extra, *d[x].shape[1:])])
+    out = torch.full(tuple(d["v"].shape), 7.0, dtype=BF, device="cuda")
+    o, pool = call(d, slots=slots, out=out)
+    d["lens"], full = [2, 3, 1], d
+    ref_o, ref_p = reference({**full, **{x: full[x][:6] for x in ("q", "k", "v", "g", "beta")}}, slots=slots)
+    assert torch.equal(o[2:5].cpu(), torch.full_like(o[2:5].cpu(), 7.0))
+    assert torch.equal(o[6:].cpu(), torch.full_like(o[6:].cpu(), 7.0))
+    assert_close("o", np64(o[:2]), ref_o[:2], tol(BF))
+    assert_close("pool", np64(pool), ref_p, TOL_F32)
+
+
+def test_strided_and_unaligned_inputs():
+    import gated_delta_rule_112_b200 as gdn
+    for dtype in (BF, F):
+        d = make([3, 8], 2, 4, 128, 64, dtype, seed=25)
+        T = 11
+        for offset in (0, 1):          # slices of one projection output, then off by one element
+            wide = torch.zeros(T, offset + 2 * 128 * 2 + 4 * 64 + 5, dtype=dtype, device="cuda")
+            q, k, v = (wide[:, offset + a:offset + a + h * w].unflatten(1, (h, w))
+                       for a, h, w in ((0, 2, 128), (256, 2, 128), (512, 4, 64)))
+            for x, name in ((q, "q"), (k, "k"), (v, "v")):
+                x.copy_(d[name])
+            pool = d["pool"].cuda()
+            o = gdn.recurrent_fwd(q, k, v, d["g"].cuda(), d["beta"].cuda(), pool, d["slots"].cuda(),
+                                  d["cu"].cuda())
+            check(d, o, pool)
+
+
+@pytest.mark.parametrize("channel", [False, True])
+def test_gates_at_their_ends(channel):
+    """g = -inf forgets everything (also what was large), strong decays, growth, beta up to 2."""
+    d = make([9, 20, 5], 1, 2, 128, 128, F, channel=channel, seed=26, gmean=3.0, beta_scale=2.0)
+    d["g"][4] = float("-inf")
+    d["g"][11:19] = -60.0             # the running product of decays underflows fp32
+    d["g"][29:33] = 1.5               # and a growing state
+    d["g"][3] = 0.0
+    o, pool = call(d)
+    check(d, o, pool)
+
+
+def test_large_pool_offsets():
+    """Slots whose elements lie past 2^32 bytes and past 2^31 elements."""
+    import gated_delta_rule_112_b200 as gdn
+    d = make([2, 1], 1, 1, 128, 128, BF, BF, seed=27, spare=0)
+    P = 140_000
+    pool = torch.empty(P, 1, 128, 128, dtype=BF, device="cuda")
+    slots = [P - 1, 131_073]
+    pool[slots] = d["pool"].cuda()
+    o = gdn.recurrent_fwd(*(d[x].cuda() for x in ("q", "k", "v", "g", "beta")), pool, ints(slots),
+                          d["cu"].cuda())
+    d["slots"] = torch.arange(2, dtype=torch.int32)
+    check(d, o, pool[slots])
+
+
+BAD = {  # what is wrong with run 1 of three: its arguments, and the runs it spoils
+    "slot_past_pool": (dict(slots=[0, 99, 2]), [1]),
+    "slot_twice": (dict(slots=[0, 2, 2]), [1, 2]),
+    "slot_twice_one_keeps": (dict(slots=[0, 2, 2], keep=[1, 0, 1]), [1, 2]),
+    "keep_past_length": (dict(keep=[1, 9, 4]), [1]),
+    "keep_negative": (dict(keep=[1, -1, 4]), [1]),
+}
+
+
+@pytest.mark.parametrize("bad", sorted(BAD))
+def test_bad_runs_are_refused(bad):
+    import gated_delta_rule_112_b200 as gdn
+    how, spoilt = BAD[bad]
+    d = make([2, 3, 4], 1, 2, 128, 128, BF, seed=28)
+    d["slots"] = torch.arange(3, dtype=torch.int32)
+    status = gdn.status_block()
+    o, pool = call(d, status=status, **how)
+    assert gdn.get_status(status) == gdn.ERR_INVALID_ARG
+    assert gdn.get_status(status) == gdn.OK                         # read once
+    ro, rp = reference(d, slots=[s if n not in spoilt else -1 for n, s in
+                                 enumerate(how.get("slots", [0, 1, 2]))],
+                       keep=None if "keep" not in how else
+                       [0 if n in spoilt else x for n, x in enumerate(how["keep"])])
+    cu = d["cu"].tolist()
+    for n in range(3):
+        rows = slice(cu[n], cu[n + 1])
+        if n in spoilt:
+            assert torch.isnan(o[rows]).all()
+        else:
+            assert_close(f"o of run {n}", np64(o[rows]), ro[rows], tol(BF))
+    assert_close("pool", np64(pool), rp, TOL_F32)
+    assert torch.equal(pool[3:].cpu(), d["pool"][3:])
+
+
+@pytest.mark.parametrize("cu", [[0, 5, 3, 9], [-2, 2, 5, 9], [0, 2, 5, 40]])
+def test_bad_boundaries_are_reported(cu):
+    import gated_delta_rule_112_b200 as gdn
+    d = make([2, 3, 4], 1, 1, 128, 128, F, seed=29)
+    d["cu"] = torch.tensor(cu, dtype=torch.int32)
+    status = gdn.status_block()
+    call(d, status=status)
+    assert gdn.get_status(status) == gdn.ERR_INVALID_ARG
+
+
+def test_runs_that_keep_nothing_may_share_a_slot():
+    import gated_delta_rule_112_b200 as gdn
+    d = make([2, 3, 4, 0], 1, 2, 128, 128, BF, seed=30)
+    status = gdn.status_block()
+    o, pool = call(d, slots=[2, 2, 2, 2], keep=[0, 0, 0, 0], status=status)
+    assert gdn.get_status(status) == gdn.OK
+    check(d, o, pool, slots=[2, 2, 2, 2], keep=[0, 0, 0, 0])
+    assert torch.equal(pool.cpu(), d["pool"])
+
+
+def test_many_runs_each_finds_its_slot():
+    """More runs than threads of a block, one slot named twice far apart."""
+    import gated_delta_rule_112_b200 as gdn
+    d = make([1] * 700, 1, 1, 32, 16, F, seed=31, spare=0)
+    slots = d["slots"].tolist()
+    status = gdn.status_block()
+    o, pool = call(d, status=status)
+    assert gdn.get_status(status) == gdn.OK
+    check(d, o, pool)
+    slots[699] = slots[3]
+    o, pool = call(d, slots=slots, status=status)
+    assert gdn.get_status(status) == gdn.ERR_INVALID_ARG
+    assert torch.isnan(o[[3, 699]]).all() and torch.isfinite(o[4:699]).all()
+
+
+def test_captured_replayed_and_on_another_stream():
+    import gated_delta_rule_112_b200 as gdn
+    d = make([3, 1, 4], 2, 4, 128, 128, BF, seed=32)
+    ref, rpool = call(d)
+    pool = d["pool"].cuda()
+    args = [d[x].cuda() for x in ("q", "k", "v", "g", "beta")]
+    slots, cu = d["slots"].cuda(), d["cu"].cuda()
+    out = torch.empty_like(ref)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o = gdn.recurrent_fwd(*args, pool, slots, cu, stream=side)
+    side.synchronize()
+    assert torch.equal(o, ref) and torch.equal(pool, rpool)
+    pool.copy_(d["pool"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.recurrent_fwd(*args, pool, slots, cu, out=out)
+    pool.copy_(d["pool"])
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref) and torch.equal(pool, rpool)
+
+
+def test_workload_pool_step_full_size():
+    """The decode workload's batch (N=256, H=32, d=128) from a pool, every state and output."""
+    d = make([1] * 256, 32, 32, 128, 128, BF, seed=33, spare=8)
+    o, pool = call(d)
+    check(d, o, pool)
