@@ -11,6 +11,7 @@ import glob
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -47,15 +48,17 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
         return lib
     obj_dir = os.path.join(HERE, "_build_checked" if checked else "_build")
     os.makedirs(obj_dir, exist_ok=True)
-    objs = []
-    for src in sources():
+    def compile_one(src):
         obj = os.path.join(obj_dir, os.path.basename(src) + ".o")
         cmd = [NVCC, *NVCC_FLAGS, *(["-DGDN_CHECKS=1"] if checked else []), "-c", src, "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
-        objs.append(obj)
+        return obj
+
+    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+        objs = list(pool.map(compile_one, sources()))
     tmp = lib + f".tmp{os.getpid()}"
     subprocess.check_call([NVCC, "-shared", "-gencode", "arch=compute_100a,code=sm_100a",
                            *objs, "-o", tmp])
