@@ -11,14 +11,20 @@
 //   dh = (w + w0) dz,   dx = r (dh - h (dh . h) / n)
 // A row is read once and written once: the kernels are bound by HBM.
 //
-// A group of G lanes (the power of two from d / 8 up) holds a row, eight
-// consecutive elements a lane, so the sums are log2 G shuffles and a pair's
-// partner is in the same lane (interleaved), G' lanes away (halves, rot a
-// multiple of 16), or fetched through a warp's own shared memory (other rot).
-// A warp takes an item: up to RPI heads of q or of k of one token. It forms
-// the item's cosines and sines once: the angle in turns is position *
-// inv_freq / 2 pi in fp64, less its whole turns, so far positions lose
-// nothing; fp32 sine and cosine of the remainder follow.
+// A group of G lanes (8, 16 or 32: from d / 8 up) holds a row, eight elements
+// a lane in two chunks of four, so the sums are log2 G shuffles. For pairs of
+// halves the chunks lie rot / 2 apart (rot a multiple of 8), otherwise side by
+// side: a pair's two elements are in one lane either way and nothing is
+// exchanged. Only halves that do not fall into chunks of four (odd rot, rows
+// off their alignment) meet in the warp's own shared memory. With
+// y = r (x C + x' S), x' the partner's element, C and S hold cosine, sine,
+// weight and scale, formed once for all heads of q and of k of a token, and the
+// row's arithmetic is 12 paired instructions for 8 elements.
+//
+// A warp takes an item: rows of one token, q's heads and then k's. It forms the
+// item's cosines and sines once: the angle in turns is position * inv_freq /
+// 2 pi in fp64, less its whole turns, so far positions lose nothing; fp32 sine
+// and cosine of the remainder follow.
 //
 // Checkpoint: 32 consecutive elements of a row share a power of two 2^e, the
 // smallest (e >= -127) with max|x| <= 448 * 2^e over the block's finite
@@ -36,7 +42,8 @@ namespace {
 constexpr int kQkThreads = 256, kQkWarps = kQkThreads / 32;
 constexpr int kMaxD = 256;
 
-enum { kPairNone, kPairInterleaved, kPairHalfLanes, kPairHalfShared };
+// How the pairs lie. Split: halves in chunks of four; shared: any halves.
+enum { kPairNone, kPairInterleaved, kPairSplit, kPairShared };
 
 struct Part {                     // q or k
   const void *x;                  // rows (dtype), or e4m3 codes
@@ -46,7 +53,7 @@ struct Part {                     // q or k
   uint8_t *codes, *scales;        // checkpoint to write, or null
   const void *w;
   int64_t x_ts, x_hs, dy_ts, dy_hs, out_ts, out_hs;
-  int H, splits;                  // heads, items per token
+  int H;                          // heads
   float scale;
 };
 
@@ -55,141 +62,176 @@ struct QkArgs {
   const int32_t *pos;
   const double *inv_freq;
   float *dw_part;                 // [2][gridDim.x][d] partial weight gradients
-  int T, d, rot, rpi, norm, lg;     // lg: log2 of the lanes of a row
+  int T, d, rot, norm;
+  int lg;                         // log2 of the lanes of a row
+  int rpi, splits;                // rows an item, items a token
   float eps, w0, rope_scale, inv_n;
 };
 
-// Eight elements of a row as they lie in memory.
+// A lane's place in a row: chunks of four elements at a and b, of which na and
+// nb exist.
+struct Lane { int a, b, na, nb; };
+template <int PAIR>
+__device__ __forceinline__ Lane lane_place(const QkArgs &A, int l) {
+  Lane L;
+  const bool split = PAIR == kPairSplit && 8 * l < A.rot;
+  L.a = split ? 4 * l : 8 * l;
+  L.b = split ? A.rot / 2 + 4 * l : 8 * l + 4;
+  L.na = max(0, min(4, A.d - L.a));
+  L.nb = max(0, min(4, A.d - L.b));
+  return L;
+}
+
+// Eight elements as they lie in memory.
 template <typename T>
 struct Raw;
 template <>
 struct Raw<__nv_bfloat16> { uint32_t w[4]; };
 template <>
 struct Raw<float> { float w[8]; };
-struct Codes { uint2 w; uint32_t e; };
+struct Codes { uint32_t w[2]; uint32_t ea, eb; };
 
-// n: how many of the eight exist; ACC: elements per access (all pointers and
-// strides are multiples of it).
+// ACC: elements an access may take; all pointers and strides are multiples of it.
 template <int ACC>
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, int n, Raw<__nv_bfloat16> &r) {
-  r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0;
-  if (ACC == 8) {
-    if (n > 0) {
-      const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
-      r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
-    }
-  } else if (ACC == 4) {
+__device__ __forceinline__ void load_chunk(const __nv_bfloat16 *p, int n, uint32_t *w) {
+  w[0] = w[1] = 0;
+  if (ACC >= 4) {
     if (n > 0) {
       const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
-      r.w[0] = v.x; r.w[1] = v.y;
-    }
-    if (n > 4) {
-      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p + 4));
-      r.w[2] = v.x; r.w[3] = v.y;
+      w[0] = v.x; w[1] = v.y;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n)
-        r.w[i / 2] |= uint32_t(*reinterpret_cast<const uint16_t *>(p + i)) << (16 * (i & 1));
+    for (int i = 0; i < 4; ++i)
+      if (i < n) w[i / 2] |= uint32_t(*reinterpret_cast<const uint16_t *>(p + i)) << (16 * (i & 1));
   }
 }
 template <int ACC>
-__device__ __forceinline__ void load8(const float *p, int n, Raw<float> &r) {
+__device__ __forceinline__ void load_chunk(const float *p, int n, float *w) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (ACC >= 4) {
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    if (n > 0) a = __ldcs(reinterpret_cast<const float4 *>(p));
-    if (n > 4) b = __ldcs(reinterpret_cast<const float4 *>(p + 4));
-    r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
-    r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
+    if (n > 0) v = __ldcs(reinterpret_cast<const float4 *>(p));
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.w[i] = i < n ? p[i] : 0.f;
+    if (n > 0) v.x = p[0];
+    if (n > 1) v.y = p[1];
+    if (n > 2) v.z = p[2];
+    if (n > 3) v.w = p[3];
+  }
+  w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+}
+template <int PAIR, int ACC>
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, const Lane &L, bool on, Raw<__nv_bfloat16> &r) {
+  if (ACC == 8 && PAIR != kPairSplit) {
+    r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0;
+    if (on && L.na > 0) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p + L.a));
+      r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    }
+  } else {
+    load_chunk<ACC>(p + L.a, on ? L.na : 0, r.w);
+    load_chunk<ACC>(p + L.b, on ? L.nb : 0, r.w + 2);
   }
 }
+template <int PAIR, int ACC>
+__device__ __forceinline__ void load8(const float *p, const Lane &L, bool on, Raw<float> &r) {
+  load_chunk<ACC>(p + L.a, on ? L.na : 0, r.w);
+  load_chunk<ACC>(p + L.b, on ? L.nb : 0, r.w + 4);
+}
 template <int ACC>
-__device__ __forceinline__ void load_codes(const uint8_t *p, const uint8_t *e, int n, Codes &r) {
-  r.w = make_uint2(0, 0);
-  r.e = n > 0 ? *e : 127;
-  if (ACC == 8) {
-    if (n > 0) r.w = __ldcs(reinterpret_cast<const uint2 *>(p));
-  } else if (ACC == 4) {
-    if (n > 0) r.w.x = __ldcs(reinterpret_cast<const uint32_t *>(p));
-    if (n > 4) r.w.y = __ldcs(reinterpret_cast<const uint32_t *>(p + 4));
+__device__ __forceinline__ uint32_t load_codes(const uint8_t *p, int n) {
+  uint32_t w = 0;
+  if (ACC >= 4) {
+    if (n > 0) w = __ldcs(reinterpret_cast<const uint32_t *>(p));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) (i < 4 ? r.w.x : r.w.y) |= uint32_t(p[i]) << (8 * (i & 3));
+    for (int i = 0; i < 4; ++i)
+      if (i < n) w |= uint32_t(p[i]) << (8 * i);
   }
+  return w;
 }
 
-__device__ __forceinline__ void unpack8(const Raw<__nv_bfloat16> &r, float (&x)[8]) {
+// The lane's elements as four pairs: chunk a, then chunk b.
+struct Row { Pair v[4]; };
+
+__device__ __forceinline__ void unpack8(const Raw<__nv_bfloat16> &r, Row &x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) { x[2 * i] = bf_lo(r.w[i]); x[2 * i + 1] = bf_hi(r.w[i]); }
+  for (int i = 0; i < 4; ++i) x.v[i] = pair(bf_lo(r.w[i]), bf_hi(r.w[i]));
 }
-__device__ __forceinline__ void unpack8(const Raw<float> &r, float (&x)[8]) {
+__device__ __forceinline__ void unpack8(const Raw<float> &r, Row &x) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = r.w[i];
+  for (int i = 0; i < 4; ++i) x.v[i] = pair(r.w[2 * i], r.w[2 * i + 1]);
 }
 // 2^(b - 127), b in [0, 254]: 2^-127 lies below the normal range.
 __device__ __forceinline__ float pow2_biased(uint32_t b) {
   return __uint_as_float(b ? b << 23 : 0x00400000u);
 }
-__device__ __forceinline__ void unpack8(const Codes &r, float (&x)[8]) {
-  const float s = pow2_biased(r.e);
+__device__ __forceinline__ void unpack8(const Codes &r, Row &x) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t w = i < 2 ? r.w.x : r.w.y;
+    const float s = pow2_biased(i < 2 ? r.ea : r.eb);
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-        static_cast<__nv_fp8x2_storage_t>((w >> (16 * (i & 1))) & 0xffff), __NV_E4M3);
+        static_cast<__nv_fp8x2_storage_t>((r.w[i / 2] >> (16 * (i & 1))) & 0xffff), __NV_E4M3);
     const float2 f = __half22float2(__half2(h));
-    x[2 * i] = f.x * s;
-    x[2 * i + 1] = f.y * s;
+    x.v[i] = mul2(pair(f.x, f.y), pair(s, s));
   }
 }
 
 template <int ACC>
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, int n, const float (&x)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = bf_pack(x[2 * i], x[2 * i + 1]);
-  if (ACC == 8) {
-    if (n > 0) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else if (ACC == 4) {
+__device__ __forceinline__ void store_chunk(__nv_bfloat16 *p, int n, Pair lo, Pair hi) {
+  const float2 f = unpair(lo), g = unpair(hi);
+  const uint32_t w[2] = {bf_pack(f.x, f.y), bf_pack(g.x, g.y)};
+  if (ACC >= 4) {
     if (n > 0) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
-    if (n > 4) *reinterpret_cast<uint2 *>(p + 4) = make_uint2(w[2], w[3]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
       if (i < n) *reinterpret_cast<uint16_t *>(p + i) = uint16_t(w[i / 2] >> (16 * (i & 1)));
   }
 }
 template <int ACC>
-__device__ __forceinline__ void store8(float *p, int n, const float (&x)[8]) {
+__device__ __forceinline__ void store_chunk(float *p, int n, Pair lo, Pair hi) {
+  const float2 f = unpair(lo), g = unpair(hi);
   if (ACC >= 4) {
-    if (n > 0) *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    if (n > 4) *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    if (n > 0) *reinterpret_cast<float4 *>(p) = make_float4(f.x, f.y, g.x, g.y);
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = x[i];
+    if (n > 0) p[0] = f.x;
+    if (n > 1) p[1] = f.y;
+    if (n > 2) p[2] = g.x;
+    if (n > 3) p[3] = g.y;
   }
 }
+template <int PAIR, int ACC>
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const Lane &L, const Row &y) {
+  if (ACC == 8 && PAIR != kPairSplit) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpair(y.v[i]);
+      w[i] = bf_pack(f.x, f.y);
+    }
+    if (L.na > 0) *reinterpret_cast<uint4 *>(p + L.a) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    store_chunk<ACC>(p + L.a, L.na, y.v[0], y.v[1]);
+    store_chunk<ACC>(p + L.b, L.nb, y.v[2], y.v[3]);
+  }
+}
+template <int PAIR, int ACC>
+__device__ __forceinline__ void store8(float *p, const Lane &L, const Row &y) {
+  store_chunk<ACC>(p + L.a, L.na, y.v[0], y.v[1]);
+  store_chunk<ACC>(p + L.b, L.nb, y.v[2], y.v[3]);
+}
 template <int ACC>
-__device__ __forceinline__ void store_codes(uint8_t *p, int n, uint2 w) {
-  if (ACC == 8) {
-    if (n > 0) *reinterpret_cast<uint2 *>(p) = w;
-  } else if (ACC == 4) {
-    if (n > 0) *reinterpret_cast<uint32_t *>(p) = w.x;
-    if (n > 4) *reinterpret_cast<uint32_t *>(p + 4) = w.y;
+__device__ __forceinline__ void store_codes(uint8_t *p, int n, uint32_t w) {
+  if (ACC >= 4) {
+    if (n > 0) *reinterpret_cast<uint32_t *>(p) = w;
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = uint8_t((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = uint8_t(w >> (8 * i));
   }
 }
 
-// Sum over the G = 2^lg lanes of a row (8, 16 or 32).
+// Sum over the 2^lg lanes of a row.
 __device__ __forceinline__ float group_sum(float x, int lg) {
   if (lg > 4) x += __shfl_xor_sync(0xffffffffu, x, 16);
   if (lg > 3) x += __shfl_xor_sync(0xffffffffu, x, 8);
@@ -197,275 +239,403 @@ __device__ __forceinline__ float group_sum(float x, int lg) {
   for (int off = 4; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
   return x;
 }
+__device__ __forceinline__ float dot8(const Row &x, const Row &y) {
+  Pair s = mul2(x.v[0], y.v[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = fma2(x.v[i], y.v[i], s);
+  const float2 f = unpair(s);
+  return f.x + f.y;
+}
 
-// The lane's share of an item's cosines and sines: c[i], s[i] for element
-// e0 + i (interleaved: for pair e0 / 2 + i), the sine signed for that element.
-struct Turn { float c[8], s[8]; };
-
+// The partner of every element of a pair. Elements that do not turn get 0:
+// their S is 0 and must not meet an infinity.
+// row: this group's part of the warp's buffer.
 template <int PAIR>
-__device__ __forceinline__ void make_turn(const QkArgs &A, int t, float sign, int e0, int lane,
-                                          float *cs, Turn &R) {
-  if (PAIR == kPairNone) return;
-  const int half = A.rot / 2;
+__device__ __forceinline__ void partners(const QkArgs &A, const Lane &L, float *row, const Row &x, Row &y) {
+  if (PAIR == kPairInterleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpair(x.v[i]);
+      const bool on = (i < 2 ? L.a : L.b) + 2 * (i & 1) < A.rot;
+      y.v[i] = on ? pair(f.y, f.x) : pair(0.f, 0.f);
+    }
+  } else if (PAIR == kPairSplit) {
+    const bool on = L.a < A.rot;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y.v[i] = on ? x.v[i ^ 2] : pair(0.f, 0.f);
+  } else if (PAIR == kPairShared) {
+    const int half = A.rot / 2;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float2 *>(row + L.a + 2 * i) = unpair(x.v[i]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 f;
+      const int e = L.a + 2 * i, g = e + 1;
+      f.x = e < A.rot ? row[e < half ? e + half : e - half] : 0.f;
+      f.y = g < A.rot ? row[g < half ? g + half : g - half] : 0.f;
+      y.v[i] = pair(f.x, f.y);
+    }
+  }
+}
+
+// The item's cosines and sines, in the warp's buffer: cs[j], cs[kMaxD / 2 + j].
+__device__ __forceinline__ void make_angles(const QkArgs &A, int t, int lane, float *cs) {
   const double p = double(A.pos[t]);
   __syncwarp();
-  for (int j = lane; j < half; j += 32) {
+  for (int j = lane; j < A.rot / 2; j += 32) {
     double turns = p * A.inv_freq[j] * 0.15915494309189533577;   // 1 / (2 pi)
     turns -= rint(turns);
     float s, c;
     sincospif(float(2.0 * turns), &s, &c);
     cs[j] = c * A.rope_scale;
-    cs[kMaxD / 2 + j] = s * A.rope_scale * sign;
+    cs[kMaxD / 2 + j] = s * A.rope_scale;
   }
   __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (PAIR == kPairInterleaved) {
-      if (i < 4) {
-        const int j = e0 / 2 + i;
-        R.c[i] = j < half ? cs[j] : 1.f;
-        R.s[i] = j < half ? cs[kMaxD / 2 + j] : 0.f;
-      }
-    } else {
-      const int e = e0 + i, j = e < half ? e : e - half;
-      const bool on = e < A.rot;
-      R.c[i] = on ? cs[j] : 1.f;
-      R.s[i] = on ? (e < half ? -cs[kMaxD / 2 + j] : cs[kMaxD / 2 + j]) : 0.f;
-    }
-  }
 }
 
+// Element i (0..7) of the lane: its place in the row, and its factors: y = x c +
+// x' s for the turn by +angle (sign 1) or -angle.
+__device__ __forceinline__ int element(const Lane &L, int i) { return i < 4 ? L.a + i : L.b + i - 4; }
 template <int PAIR>
-__device__ __forceinline__ void turn8(const QkArgs &A, const Turn &R, int e0, int lane, float *row,
-                                      float (&z)[8]) {
-  if (PAIR == kPairInterleaved) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = z[2 * i], b = z[2 * i + 1];
-      if (e0 + 2 * i < A.rot) {
-        z[2 * i] = a * R.c[i] - b * R.s[i];
-        z[2 * i + 1] = b * R.c[i] + a * R.s[i];
-      }
-    }
-  } else if (PAIR == kPairHalfLanes) {
-    const int off = A.rot / 16;
-    const int src = e0 < A.rot / 2 ? lane + off : e0 < A.rot ? lane - off : lane;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_sync(0xffffffffu, z[i], src);
-      if (e0 < A.rot) z[i] = z[i] * R.c[i] + o * R.s[i];
-    }
-  } else if (PAIR == kPairHalfShared) {   // row: this group's part of the warp's buffer
-    const int half = A.rot / 2;
-    __syncwarp();
-    *reinterpret_cast<float4 *>(row + e0) = make_float4(z[0], z[1], z[2], z[3]);
-    *reinterpret_cast<float4 *>(row + e0 + 4) = make_float4(z[4], z[5], z[6], z[7]);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = e0 + i;
-      if (e < A.rot) z[i] = z[i] * R.c[i] + row[e < half ? e + half : e - half] * R.s[i];
-    }
-  }
+__device__ __forceinline__ void factors(const QkArgs &A, const Lane &L, const float *cs, int i, float sign,
+                                        float &c, float &s) {
+  c = 1.f;
+  s = 0.f;
+  const int e = element(L, i), half = A.rot / 2;
+  if (PAIR == kPairNone || e >= A.rot) return;
+  const bool first = PAIR == kPairInterleaved ? !(i & 1) : e < half;
+  const int j = PAIR == kPairInterleaved ? e / 2 : first ? e : e - half;
+  c = cs[j];
+  s = first ? -sign * cs[kMaxD / 2 + j] : sign * cs[kMaxD / 2 + j];
 }
 
 __device__ __forceinline__ float rnorm(const QkArgs &A, float ss) {
   return A.norm == GDN_NORM_NONE ? 1.f : rsqrtf(ss * A.inv_n + A.eps);
 }
 
-template <typename T, int ACC>
-__device__ __forceinline__ void load_w(const QkArgs &A, const Part &P, int e0, int n, float (&w)[8]) {
-  if (P.w) {
-    const T *p = static_cast<const T *>(P.w) + e0;
+// w + w0 of the lane's elements, 1 without weights.
+template <typename T>
+__device__ __forceinline__ void load_w(const QkArgs &A, const Part &P, const Lane &L, float (&w)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = i < n ? to_f32(p[i]) + A.w0 : 0.f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.f;
+  for (int i = 0; i < 8; ++i) {
+    w[i] = 1.f;
+    const int e = element(L, i);
+    if (P.w && e < A.d) w[i] = to_f32(static_cast<const T *>(P.w)[e]) + A.w0;
   }
-}
-
-// Where an item's rows are.
-struct Item { int t, h0, h1; };
-__device__ __forceinline__ Item item_at(const QkArgs &A, const Part &P, int64_t item) {
-  Item I;
-  I.t = int(item / P.splits);
-  I.h0 = int(item % P.splits) * A.rpi;
-  I.h1 = min(P.H, I.h0 + A.rpi);
-  return I;
 }
 
 // Source of the rows: T in memory, or codes.
-template <typename T, bool PACKED, int ACC>
+template <typename T, bool PACKED, int PAIR, int ACC>
 struct Source {
   Raw<T> raw;
-  __device__ __forceinline__ void load(const QkArgs &, const Part &P, int t, int h, int e0, int n) {
-    load8<ACC>(static_cast<const T *>(P.x) + t * P.x_ts + h * P.x_hs + e0, n, raw);
+  __device__ __forceinline__ void load(const QkArgs &, const Part &P, int64_t t, int h, const Lane &L, bool on) {
+    load8<PAIR, ACC>(static_cast<const T *>(P.x) + t * P.x_ts + h * P.x_hs, L, on, raw);
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const { unpack8(raw, x); }
 };
-template <typename T, int ACC>
-struct Source<T, true, ACC> {
+template <typename T, int PAIR, int ACC>
+struct Source<T, true, PAIR, ACC> {
   Codes raw;
-  __device__ __forceinline__ void load(const QkArgs &A, const Part &P, int t, int h, int e0, int n) {
-    const int64_t row = int64_t(t) * P.H + h;
-    load_codes<ACC>(static_cast<const uint8_t *>(P.x) + row * A.d + e0,
-                    P.x_scales + row * ((A.d + 31) / 32) + e0 / 32, n, raw);
+  __device__ __forceinline__ void load(const QkArgs &A, const Part &P, int64_t t, int h, const Lane &L, bool on) {
+    const int64_t row = t * P.H + h;
+    const uint8_t *p = static_cast<const uint8_t *>(P.x) + row * A.d;
+    const uint8_t *e = P.x_scales + row * ((A.d + 31) / 32);
+    if (ACC == 8 && PAIR != kPairSplit) {
+      raw.w[0] = raw.w[1] = 0;
+      raw.ea = 127;
+      if (on && L.na > 0) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p + L.a));
+        raw.w[0] = v.x; raw.w[1] = v.y;
+        raw.ea = e[L.a / 32];
+      }
+      raw.eb = raw.ea;
+    } else {
+      raw.w[0] = load_codes<ACC>(p + L.a, on ? L.na : 0);
+      raw.w[1] = load_codes<ACC>(p + L.b, on ? L.nb : 0);
+      raw.ea = on && L.na > 0 ? e[L.a / 32] : 127;
+      raw.eb = on && L.nb > 0 ? e[L.b / 32] : 127;
+    }
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const { unpack8(raw, x); }
 };
 
-template <int ACC>
-__device__ __forceinline__ void write_codes(const QkArgs &A, const Part &P, int64_t row, int e0, int n,
-                                            bool on, const float (&x)[8]) {
-  float top = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = fabsf(x[i]);
-    top = fmaxf(top, a <= 3.402823466e38f ? a : 0.f);     // false for infinities and NaN
-  }
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  // 448 = 1.75 * 2^8: e = exponent - 8, and one more where the significand is above 1.75
+// The biased exponent that a block's largest finite magnitude asks for. 448 =
+// 1.75 * 2^8: its exponent - 8, and one more where the significand is above 1.75.
+__device__ __forceinline__ int block_exponent(float top) {
   const uint32_t bits = __float_as_uint(top);
-  const int be = max(int(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), 0);
+  return max(int((bits + 0x1fffffu) >> 23) - 8, 0);
+}
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a <= 3.402823466e38f ? a : 0.f;                // false for infinities and NaN
+}
+__device__ __forceinline__ uint32_t encode4(Pair lo, Pair hi, int be) {
   const float inv = __uint_as_float(uint32_t(254 - be) << 23);     // 2^-(be - 127)
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float2 v = make_float2(x[2 * i] * inv, x[2 * i + 1] * inv);
-    v.x = fabsf(x[2 * i]) <= 3.402823466e38f ? v.x : __int_as_float(0x7fffffff);
-    v.y = fabsf(x[2 * i + 1]) <= 3.402823466e38f ? v.y : __int_as_float(0x7fffffff);
-    c[i] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-  }
-  if (!on) return;
-  store_codes<ACC>(P.codes + row * A.d + e0, n, make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16));
-  if ((e0 & 31) == 0 && n > 0) P.scales[row * ((A.d + 31) / 32) + e0 / 32] = uint8_t(be);
+  const float2 a = unpair(mul2(lo, pair(inv, inv))), b = unpair(mul2(hi, pair(inv, inv)));
+  return __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
+         uint32_t(__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3)) << 16;
 }
 
-template <typename T, bool PACKED, int PAIR, int ACC>
-__global__ void __launch_bounds__(kQkThreads) gdn_qk_fwd_kernel(const __grid_constant__ QkArgs A) {
+// Writes the lane's eight elements in 8 bits. Side by side, four lanes hold a
+// block; with halves in chunks eight lanes' first chunks do, and their second
+// chunks, where rot / 2 is a multiple of 32; for other rot the blocks' maxima
+// meet in shared memory (of non-negative floats the bits compare alike).
+template <int PAIR, int ACC>
+__device__ __forceinline__ void write_codes(const QkArgs &A, const Part &P, int64_t row, const Lane &L,
+                                            bool on, float *row_buf, const Row &x) {
+  float t[2];
+  bool fine = true;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 f = unpair(x.v[2 * i]), g = unpair(x.v[2 * i + 1]);
+    t[i] = fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(g.x), fabsf(g.y)));
+    fine &= f.x - f.x == 0.f && f.y - f.y == 0.f && g.x - g.x == 0.f && g.y - g.y == 0.f;
+  }
+  Row z = x;
+  if (!fine) {                          // what is not finite counts for nothing, and becomes NaN
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      t[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float2 f = unpair(x.v[2 * i + k]);
+        t[i] = fmaxf(t[i], fmaxf(finite_abs(f.x), finite_abs(f.y)));
+        if (f.x - f.x != 0.f) f.x = __int_as_float(0x7fffffff);
+        if (f.y - f.y != 0.f) f.y = __int_as_float(0x7fffffff);
+        z.v[2 * i + k] = pair(f.x, f.y);
+      }
+    }
+  }
+  const bool split = PAIR == kPairSplit && L.a < A.rot;
+  if (PAIR == kPairSplit && A.rot % 64) {
+    uint32_t *top = reinterpret_cast<uint32_t *>(row_buf);
+    __syncwarp();
+    if ((L.a & 31) == 0) top[L.a / 32] = 0;
+    if ((L.b & 31) == 0) top[L.b / 32] = 0;
+    __syncwarp();
+    atomicMax(&top[L.a / 32], __float_as_uint(t[0]));
+    atomicMax(&top[L.b / 32], __float_as_uint(t[1]));
+    __syncwarp();
+    t[0] = __uint_as_float(top[L.a / 32]);
+    t[1] = __uint_as_float(top[L.b / 32]);
+  } else {
+    if (!split) t[0] = t[1] = fmaxf(t[0], t[1]);
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      t[0] = fmaxf(t[0], __shfl_xor_sync(0xffffffffu, t[0], off));
+      if (PAIR == kPairSplit) t[1] = fmaxf(t[1], __shfl_xor_sync(0xffffffffu, t[1], off));
+    }
+    if (PAIR == kPairSplit) {
+      const float u0 = __shfl_xor_sync(0xffffffffu, t[0], 4), u1 = __shfl_xor_sync(0xffffffffu, t[1], 4);
+      if (split) { t[0] = fmaxf(t[0], u0); t[1] = fmaxf(t[1], u1); }
+    }
+  }
+  const int ea = block_exponent(t[0]), eb = PAIR == kPairSplit ? block_exponent(t[1]) : ea;
+  const uint32_t ca = encode4(z.v[0], z.v[1], ea), cb = encode4(z.v[2], z.v[3], eb);
+  if (!on) return;
+  uint8_t *p = P.codes + row * A.d, *e = P.scales + row * ((A.d + 31) / 32);
+  if (ACC == 8 && PAIR != kPairSplit) {
+    if (L.na > 0) *reinterpret_cast<uint2 *>(p + L.a) = make_uint2(ca, cb);
+  } else {
+    store_codes<ACC>(p + L.a, L.na, ca);
+    store_codes<ACC>(p + L.b, L.nb, cb);
+  }
+  if ((L.a & 31) == 0 && L.na > 0) e[L.a / 32] = uint8_t(ea);
+  if (PAIR == kPairSplit && (L.b & 31) == 0 && L.nb > 0) e[L.b / 32] = uint8_t(eb);
+}
+
+// Where a warp's item lies.
+struct Item { int t, r0, r1; };
+__device__ __forceinline__ Item item_at(const QkArgs &A, int64_t item) {
+  Item I;
+  I.t = int(A.splits == 1 ? item : item / A.splits);
+  I.r0 = int(item - int64_t(I.t) * A.splits) * A.rpi;
+  I.r1 = min(A.p[0].H + A.p[1].H, I.r0 + A.rpi);
+  return I;
+}
+
+// PACK: also write codes.
+template <typename T, bool PACKED, bool PACK, int PAIR, int ACC>
+__global__ void __launch_bounds__(kQkThreads, 3) gdn_qk_fwd_kernel(const __grid_constant__ QkArgs A) {
   constexpr int U = 4;
-  const int G = 1 << A.lg, R = 32 >> A.lg;
   __shared__ float cs_all[PAIR == kPairNone ? 1 : kQkWarps][kMaxD];
-  __shared__ __align__(16) float rows_all[PAIR == kPairHalfShared ? kQkWarps : 1][kMaxD];
+  constexpr bool kRows = PAIR == kPairShared || (PACK && PAIR == kPairSplit);
+  __shared__ __align__(16) float rows_all[kRows ? kQkWarps : 1][kMaxD];
+  const int G = 1 << A.lg, R = 32 >> A.lg;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> A.lg;
   float *cs = cs_all[PAIR == kPairNone ? 0 : warp];
-  float *row_buf = rows_all[PAIR == kPairHalfShared ? warp : 0] + (lane & -G) * 8;
-  const int e0 = (lane & (G - 1)) * 8, n = max(0, min(8, A.d - e0));
-  const int64_t nwarps = int64_t(gridDim.x) * kQkWarps;
-  for (int part = 0; part < 2; ++part) {
-    const Part &P = A.p[part];
-    const int64_t items = int64_t(A.T) * P.splits;
-    float w[8];
-    load_w<T, ACC>(A, P, e0, n, w);
-    for (int64_t item = int64_t(blockIdx.x) * kQkWarps + warp; item < items; item += nwarps) {
-      const Item I = item_at(A, P, item);
-      Turn turn;
-      make_turn<PAIR>(A, I.t, 1.f, e0, lane, cs, turn);
-      for (int h0 = I.h0; h0 < I.h1; h0 += R * U) {
-        Source<T, PACKED, ACC> src[U];
+  float *row_buf = rows_all[kRows ? warp : 0] + (lane & -G) * 8;
+  const Lane L = lane_place<PAIR>(A, lane & (G - 1));
+  const int64_t nwarps = int64_t(gridDim.x) * kQkWarps, items = int64_t(A.T) * A.splits;
+  for (int64_t item = int64_t(blockIdx.x) * kQkWarps + warp; item < items; item += nwarps) {
+    const Item I = item_at(A, item);
+    if (PAIR != kPairNone) make_angles(A, I.t, lane, cs);
+    for (int part = 0; part < 2; ++part) {
+      const Part &P = A.p[part];
+      const int first = part ? A.p[0].H : 0;
+      const int h0 = max(I.r0 - first, 0), h1 = min(I.r1 - first, P.H);
+      if (h0 >= h1) continue;
+      Row C, S;
+      {
+        float w[8];
+        load_w<T>(A, P, L, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float c0, c1, s0, s1;
+          factors<PAIR>(A, L, cs, 2 * i, 1.f, c0, s0);
+          factors<PAIR>(A, L, cs, 2 * i + 1, 1.f, c1, s1);
+          C.v[i] = pair(c0 * w[2 * i] * P.scale, c1 * w[2 * i + 1] * P.scale);
+          S.v[i] = pair(s0 * P.scale, s1 * P.scale);
+        }
+        if (P.w && PAIR != kPairNone) {         // S takes the partner's weight
+          Row v, u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v.v[i] = pair(w[2 * i], w[2 * i + 1]);
+          partners<PAIR>(A, L, row_buf, v, u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) S.v[i] = mul2(S.v[i], u.v[i]);
+        }
+      }
+      for (int h = h0; h < h1; h += R * U) {
+        Source<T, PACKED, PAIR, ACC> src[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int h = h0 + u * R + sub;
-          src[u].load(A, P, I.t, h < I.h1 ? h : I.h0, e0, h < I.h1 ? n : 0);
+          const int hu = h + u * R + sub;
+          src[u].load(A, P, I.t, hu < h1 ? hu : h0, L, hu < h1);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (h0 + u * R >= I.h1) break;
-          const int h = h0 + u * R + sub;
-          const bool on = h < I.h1;
-          float x[8];
-          src[u].get(x);
-          if (!PACKED && P.codes)
-            write_codes<ACC>(A, P, int64_t(I.t) * P.H + h, e0, n, on, x);
-          float ss = 0.f;
+          if (h + u * R >= h1) break;
+          const int hu = h + u * R + sub;
+          const bool on = hu < h1;
+          Row x, y;
+          unpack8(src[u].raw, x);
+          if (PACK && P.codes) write_codes<PAIR, ACC>(A, P, int64_t(I.t) * P.H + hu, L, on, row_buf, x);
+          if (PACK && !P.out) continue;
+          if (A.norm != GDN_NORM_NONE) {
+            const float r = rnorm(A, group_sum(dot8(x, x), A.lg));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-          const float r = rnorm(A, group_sum(ss, A.lg));
+            for (int i = 0; i < 4; ++i) x.v[i] = mul2(x.v[i], pair(r, r));
+          }
+          if (PAIR != kPairNone) {
+            partners<PAIR>(A, L, row_buf, x, y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-          turn8<PAIR>(A, turn, e0, lane, row_buf, x);
+            for (int i = 0; i < 4; ++i) x.v[i] = fma2(y.v[i], S.v[i], mul2(x.v[i], C.v[i]));
+          } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] *= P.scale;
-          if (on && P.out)
-            store8<ACC>(static_cast<T *>(P.out) + I.t * P.out_ts + h * P.out_hs + e0, n, x);
+            for (int i = 0; i < 4; ++i) x.v[i] = mul2(x.v[i], C.v[i]);
+          }
+          if (on) store8<PAIR, ACC>(static_cast<T *>(P.out) + I.t * P.out_ts + hu * P.out_hs, L, x);
         }
       }
     }
   }
 }
 
-template <typename T, typename DT, bool PACKED, int PAIR, int ACC>
-__global__ void __launch_bounds__(kQkThreads) gdn_qk_bwd_kernel(const __grid_constant__ QkArgs A) {
+// WEIGHTS: weights and their gradients.
+template <typename T, typename DT, bool PACKED, bool WEIGHTS, int PAIR, int ACC>
+__global__ void __launch_bounds__(kQkThreads, 2) gdn_qk_bwd_kernel(const __grid_constant__ QkArgs A) {
   constexpr int U = 2;
-  const int G = 1 << A.lg, R = 32 >> A.lg;
   __shared__ float cs_all[PAIR == kPairNone ? 1 : kQkWarps][kMaxD];
-  __shared__ __align__(16) float rows_all[kQkWarps][kMaxD];
+  __shared__ __align__(16) float rows_all[PAIR == kPairShared || WEIGHTS ? kQkWarps : 1][kMaxD];
+  const int G = 1 << A.lg, R = 32 >> A.lg;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> A.lg;
   float *cs = cs_all[PAIR == kPairNone ? 0 : warp];
-  float *row_buf = rows_all[warp] + (lane & -G) * 8;
-  const int e0 = (lane & (G - 1)) * 8, n = max(0, min(8, A.d - e0));
-  const int64_t nwarps = int64_t(gridDim.x) * kQkWarps;
-  for (int part = 0; part < 2; ++part) {
-    const Part &P = A.p[part];
-    const int64_t items = int64_t(A.T) * P.splits;
-    float w[8], dw[8];
-    load_w<T, ACC>(A, P, e0, n, w);
+  float *row_buf = rows_all[PAIR == kPairShared || WEIGHTS ? warp : 0] + (lane & -G) * 8;
+  const Lane L = lane_place<PAIR>(A, lane & (G - 1));
+  const int64_t nwarps = int64_t(gridDim.x) * kQkWarps, items = int64_t(A.T) * A.splits;
+  Row dw[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[i] = 0.f;
-    for (int64_t item = int64_t(blockIdx.x) * kQkWarps + warp; item < items; item += nwarps) {
-      const Item I = item_at(A, P, item);
-      Turn turn;
-      make_turn<PAIR>(A, I.t, -1.f, e0, lane, cs, turn);
-      for (int h0 = I.h0; h0 < I.h1; h0 += R * U) {
-        Source<T, PACKED, ACC> src[U];
+  for (int i = 0; i < 8; ++i) dw[i / 4].v[i % 4] = pair(0.f, 0.f);
+  for (int64_t item = int64_t(blockIdx.x) * kQkWarps + warp; item < items; item += nwarps) {
+    const Item I = item_at(A, item);
+    if (PAIR != kPairNone) make_angles(A, I.t, lane, cs);
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const Part &P = A.p[part];
+      const int first = part ? A.p[0].H : 0;
+      const int h0 = max(I.r0 - first, 0), h1 = min(I.r1 - first, P.H);
+      if (h0 >= h1) continue;
+      Row C, S, W;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float c0, c1, s0, s1;
+        factors<PAIR>(A, L, cs, 2 * i, -1.f, c0, s0);
+        factors<PAIR>(A, L, cs, 2 * i + 1, -1.f, c1, s1);
+        C.v[i] = pair(c0 * P.scale, c1 * P.scale);
+        S.v[i] = pair(s0 * P.scale, s1 * P.scale);
+      }
+      if (WEIGHTS) {
+        float w[8];
+        load_w<T>(A, P, L, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) W.v[i] = pair(w[2 * i], w[2 * i + 1]);
+      }
+      for (int h = h0; h < h1; h += R * U) {
+        Source<T, PACKED, PAIR, ACC> src[U];
         Raw<DT> grad[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int h = h0 + u * R + sub;
-          const bool on = h < I.h1;
-          src[u].load(A, P, I.t, on ? h : I.h0, e0, on ? n : 0);
-          load8<ACC>(static_cast<const DT *>(P.dy) + I.t * P.dy_ts + (on ? h : I.h0) * P.dy_hs + e0,
-                     on ? n : 0, grad[u]);
+          const int hu = h + u * R + sub;
+          const bool on = hu < h1;
+          src[u].load(A, P, I.t, on ? hu : h0, L, on);
+          load8<PAIR, ACC>(static_cast<const DT *>(P.dy) + I.t * P.dy_ts + (on ? hu : h0) * P.dy_hs, L, on,
+                           grad[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (h0 + u * R >= I.h1) break;
-          const int h = h0 + u * R + sub;
-          float x[8], z[8];
-          src[u].get(x);
+          if (h + u * R >= h1) break;
+          const int hu = h + u * R + sub;
+          Row x, z, y;
+          unpack8(src[u].raw, x);
           unpack8(grad[u], z);
+          if (PAIR != kPairNone) {
+            partners<PAIR>(A, L, row_buf, z, y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] *= P.scale;
-          turn8<PAIR>(A, turn, e0, lane, row_buf, z);
-          float ss = 0.f, dot = 0.f;
+            for (int i = 0; i < 4; ++i) z.v[i] = fma2(y.v[i], S.v[i], mul2(z.v[i], C.v[i]));
+          } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) { ss += x[i] * x[i]; dot += z[i] * w[i] * x[i]; }
-          const float r = rnorm(A, group_sum(ss, A.lg));
-          const float m = A.norm == GDN_NORM_NONE ? 0.f : group_sum(dot, A.lg) * r * A.inv_n;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float hx = x[i] * r;
-            if (P.w) dw[i] += z[i] * hx;
-            x[i] = A.norm == GDN_NORM_NONE ? z[i] * w[i] : r * (z[i] * w[i] - hx * m);
+            for (int i = 0; i < 4; ++i) z.v[i] = mul2(z.v[i], C.v[i]);
           }
-          if (h < I.h1)
-            store8<ACC>(static_cast<T *>(P.out) + I.t * P.out_ts + h * P.out_hs + e0, n, x);
+          float r = 1.f, m = 0.f;
+          Row dh = z;
+          if (WEIGHTS) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dh.v[i] = mul2(z.v[i], W.v[i]);
+          }
+          if (A.norm != GDN_NORM_NONE) {
+            r = rnorm(A, group_sum(dot8(x, x), A.lg));
+            m = group_sum(dot8(x, dh), A.lg) * r * A.inv_n;
+          }
+          const Pair rr = pair(r, r), mm = pair(-m, -m);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const Pair hx = mul2(x.v[i], rr);
+            if (WEIGHTS) dw[part].v[i] = fma2(z.v[i], hx, dw[part].v[i]);
+            x.v[i] = A.norm == GDN_NORM_NONE ? dh.v[i] : mul2(fma2(hx, mm, dh.v[i]), rr);
+          }
+          if (hu < h1) store8<PAIR, ACC>(static_cast<T *>(P.out) + I.t * P.out_ts + hu * P.out_hs, L, x);
         }
       }
     }
-    if (P.w) {      // the block's rows in a fixed order: warps 0..7, and in each its groups
+  }
+  if (WEIGHTS) {    // the block's rows in a fixed order: warps 0..7, and in each its groups
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) row_buf[e0 + i] = dw[i];
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = unpair(dw[part].v[i / 2]);
+        const int e = element(L, i);
+        if (e < G * 8) row_buf[e] = i & 1 ? f.y : f.x;
+      }
       __syncthreads();
       for (int e = threadIdx.x; e < A.d; e += kQkThreads) {
         float s = 0.f;
         for (int i = 0; i < kQkWarps * R; ++i) s += rows_all[i / R][(i % R) * G * 8 + e];
         A.dw_part[(int64_t(part) * gridDim.x + blockIdx.x) * A.d + e] = s;
       }
-      __syncthreads();
     }
   }
 }
@@ -508,45 +678,53 @@ int access_width(const QkArgs &A, size_t xe, size_t dye, bool packed) {
   return 1;
 }
 
-int pair_mode(const gdn_qk_params *p) {
+// The way the pairs are handled: halves go in chunks where they fall into them.
+int pair_mode(const gdn_qk_params *p, int acc) {
   if (!p->rot) return kPairNone;
   if (p->interleaved) return kPairInterleaved;
-  return p->rot % 16 == 0 ? kPairHalfLanes : kPairHalfShared;
+  return acc >= 4 && p->rot % 8 == 0 ? kPairSplit : kPairShared;
 }
 
-// Blocks of a launch over `items` warps' worth of work.
-unsigned grid_for(int64_t items, int sms, int per_sm) {
-  const int64_t blocks = (items + kQkWarps - 1) / kQkWarps, most = int64_t(sms) * per_sm;
+constexpr int kFwdBlocksPerSm = 3, kBwdBlocksPerSm = 2;
+
+// Rows an item and items a token: whole tokens, whose cosines then serve every
+// head, where there are enough of them for all warps; else fewer rows, down to
+// one step of a warp.
+unsigned plan(QkArgs &A, int per_sm) {
+  const int rows = A.p[0].H + A.p[1].H, step = 32 >> A.lg, sms = device_sms();
+  const int64_t warps = int64_t(sms > 0 ? sms : 1) * per_sm * kQkWarps;
+  int64_t want = (int64_t(A.T) * rows + warps - 1) / warps;          // rows a warp
+  want = (want + step - 1) / step * step;
+  A.rpi = int(want < 1 ? 1 : want < rows ? want : rows > 0 ? rows : 1);
+  A.splits = (rows + A.rpi - 1) / A.rpi;
+  const int64_t blocks = (int64_t(A.T) * A.splits + kQkWarps - 1) / kQkWarps;
+  const int64_t most = int64_t(sms > 0 ? sms : 1) * per_sm;
   return unsigned(blocks < 1 ? 1 : blocks < most ? blocks : most);
 }
 
-constexpr int kFwdBlocksPerSm = 4, kBwdBlocksPerSm = 4;
-
-// Turns the run-time choices into template arguments. A variant for each way
-// the pairs lie, at the widest access (16 bytes of T); narrower accesses, which
-// unaligned rows take, share partners through shared memory in every case of
-// halves.
+// Turns the run-time choices into template arguments: a variant for each way
+// the pairs lie, at the widest access (16 bytes of T where eight elements lie
+// side by side) and narrower ones.
 template <int V> struct Const { static constexpr int value = V; };
 template <typename T, typename F>
 void with_variant(int pair, int acc, F f) {
-  constexpr int wide = sizeof(T) == 2 ? 8 : 4;
   auto pick = [&](auto a) {
     if (pair == kPairNone) f(Const<kPairNone>{}, a);
     else if (pair == kPairInterleaved) f(Const<kPairInterleaved>{}, a);
-    else f(Const<kPairHalfShared>{}, a);
+    else f(Const<kPairShared>{}, a);
   };
-  if (acc >= wide && pair == kPairHalfLanes) f(Const<kPairHalfLanes>{}, Const<wide>{});
-  else if (acc >= wide) pick(Const<wide>{});
+  if (pair == kPairSplit) f(Const<kPairSplit>{}, Const<4>{});
+  else if (acc == 8 && sizeof(T) == 2) pick(Const<8>{});
   else if (acc >= 4) pick(Const<4>{});
   else pick(Const<1>{});
 }
 
-template <bool PACKED>
+template <bool PACKED, bool PACK>
 cudaError_t fwd_launch(const QkArgs &A, int dtype, int pair, int acc, unsigned grid, cudaStream_t s) {
   auto go = [&](auto type) {
     using T = decltype(type);
     with_variant<T>(pair, acc, [&](auto p, auto a) {
-      gdn_qk_fwd_kernel<T, PACKED, decltype(p)::value, decltype(a)::value>
+      gdn_qk_fwd_kernel<T, PACKED, PACK, decltype(p)::value, decltype(a)::value>
           <<<grid, kQkThreads, 0, s>>>(A);
     });
   };
@@ -554,14 +732,14 @@ cudaError_t fwd_launch(const QkArgs &A, int dtype, int pair, int acc, unsigned g
   else go(float{});
   return cudaGetLastError();
 }
-template <bool PACKED>
+template <bool PACKED, bool WEIGHTS>
 cudaError_t bwd_launch(const QkArgs &A, int dtype, int grad_dtype, int pair, int acc, unsigned grid,
                        cudaStream_t s) {
   auto go = [&](auto type, auto grad) {
     using T = decltype(type);
     using DT = decltype(grad);
     with_variant<T>(pair, acc, [&](auto p, auto a) {
-      gdn_qk_bwd_kernel<T, DT, PACKED, decltype(p)::value, decltype(a)::value>
+      gdn_qk_bwd_kernel<T, DT, PACKED, WEIGHTS, decltype(p)::value, decltype(a)::value>
           <<<grid, kQkThreads, 0, s>>>(A);
     });
   };
@@ -630,17 +808,7 @@ int fill(QkArgs &A, const gdn_qk_params *p, const gdn_rows *const x[2],
       return GDN_ERR_INVALID_ARG;
     }
   }
-  // Heads per item: enough items for every warp of the device where there are
-  // tokens enough, else one step of a warp.
-  A.rpi = 16;
-  for (Part &P : A.p) P.splits = (P.H + A.rpi - 1) / A.rpi;
   return GDN_OK;
-}
-
-int64_t total_items(const QkArgs &A) {
-  int64_t most = 0;
-  for (const Part &P : A.p) most = most < int64_t(A.T) * P.splits ? int64_t(A.T) * P.splits : most;
-  return most;
 }
 
 template <bool PACKED>
@@ -651,11 +819,16 @@ int run_fwd(const gdn_qk_params *p, const gdn_rows *const x[2], const gdn_packed
   QkArgs A{};
   rc = fill(A, p, x, PACKED ? x8 : nullptr, nullptr, 0, out, out8);
   if (rc != GDN_OK) return rc;
-  if (total_items(A) == 0) return GDN_OK;
-  const unsigned grid = grid_for(total_items(A), device_sms(), kFwdBlocksPerSm);
+  if (!A.p[0].H && !A.p[1].H) return GDN_OK;
+  const bool pack = A.p[0].codes || A.p[1].codes;
+  const unsigned grid = plan(A, kFwdBlocksPerSm);
   const int acc = access_width(A, p->dtype == GDN_BF16 ? 2 : 4, 2, PACKED);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = fwd_launch<PACKED>(A, p->dtype, pair_mode(p), acc, grid, s);
+  const int pair = pair_mode(p, acc);
+  cudaError_t e;
+  if constexpr (PACKED) e = fwd_launch<true, false>(A, p->dtype, pair, acc, grid, s);
+  else if (pack) e = fwd_launch<false, true>(A, p->dtype, pair, acc, grid, s);
+  else e = fwd_launch<false, false>(A, p->dtype, pair, acc, grid, s);
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -675,13 +848,15 @@ int run_bwd(const gdn_qk_params *p, const gdn_rows *const dy[2], int grad_dtype,
   rc = fill(A, p, x, PACKED ? x8 : nullptr, dy, grad_dtype == GDN_BF16 ? 2 : 4, out, nullptr);
   if (rc != GDN_OK) return rc;
   A.dw_part = static_cast<float *>(ws);
-  const unsigned grid = grid_for(total_items(A), device_sms(), kBwdBlocksPerSm);
+  const unsigned grid = plan(A, kBwdBlocksPerSm);
   const int acc = access_width(A, p->dtype == GDN_BF16 ? 2 : 4, grad_dtype == GDN_BF16 ? 2 : 4, PACKED);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (total_items(A) > 0 || dw_q || dw_k) {
-    const cudaError_t e = bwd_launch<PACKED>(A, p->dtype, grad_dtype, pair_mode(p), acc, grid, s);
-    if (e != cudaSuccess) return GDN_ERR_CUDA;
-  }
+  if (!A.p[0].H && !A.p[1].H && !dw_q && !dw_k) return GDN_OK;
+  const int pair = pair_mode(p, acc);
+  const cudaError_t e =
+      dw_q || dw_k ? bwd_launch<PACKED, true>(A, p->dtype, grad_dtype, pair, acc, grid, s)
+                   : bwd_launch<PACKED, false>(A, p->dtype, grad_dtype, pair, acc, grid, s);
+  if (e != cudaSuccess) return GDN_ERR_CUDA;
   if (dw_q || dw_k) {
     gdn_qk_dw_kernel<<<dim3((p->d + 31) / 32, 2), 1024, 0, s>>>(A.dw_part, int(grid), p->d, dw_q, dw_k);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
