@@ -247,22 +247,26 @@ __device__ __forceinline__ float dot8(const Row &x, const Row &y) {
   return f.x + f.y;
 }
 
-// The partner of every element of a pair. Elements that do not turn get 0:
-// their S is 0 and must not meet an infinity.
+// The lane's part of y = x C + x' S, x' the partner of every element. What does
+// not turn takes no partner: it must not meet another element's infinity.
 // row: this group's part of the warp's buffer.
 template <int PAIR>
-__device__ __forceinline__ void partners(const QkArgs &A, const Lane &L, float *row, const Row &x, Row &y) {
+__device__ __forceinline__ void turn(const QkArgs &A, const Lane &L, float *row, const Row &C, const Row &S,
+                                     Row &x) {
+  Row y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y.v[i] = mul2(x.v[i], C.v[i]);
   if (PAIR == kPairInterleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = unpair(x.v[i]);
-      const bool on = (i < 2 ? L.a : L.b) + 2 * (i & 1) < A.rot;
-      y.v[i] = on ? pair(f.y, f.x) : pair(0.f, 0.f);
+      if (L.a + 2 * i < A.rot) y.v[i] = fma2(pair(f.y, f.x), S.v[i], y.v[i]);
     }
   } else if (PAIR == kPairSplit) {
-    const bool on = L.a < A.rot;
+    if (L.a < A.rot) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y.v[i] = on ? x.v[i ^ 2] : pair(0.f, 0.f);
+      for (int i = 0; i < 4; ++i) y.v[i] = fma2(x.v[i ^ 2], S.v[i], y.v[i]);
+    }
   } else if (PAIR == kPairShared) {
     const int half = A.rot / 2;
     __syncwarp();
@@ -276,99 +280,152 @@ __device__ __forceinline__ void partners(const QkArgs &A, const Lane &L, float *
       const int e = L.a + 2 * i, g = e + 1;
       f.x = e < A.rot ? row[e < half ? e + half : e - half] : 0.f;
       f.y = g < A.rot ? row[g < half ? g + half : g - half] : 0.f;
-      y.v[i] = pair(f.x, f.y);
+      y.v[i] = fma2(pair(f.x, f.y), S.v[i], y.v[i]);
     }
   }
+  x = y;
 }
 
-// The item's cosines and sines, in the warp's buffer: cs[j], cs[kMaxD / 2 + j].
+// The item's cosines and sines, in the warp's buffer: cs[j], cs[kMaxD / 2 + j];
+// 1 and 0 for the pairs that do not turn.
 __device__ __forceinline__ void make_angles(const QkArgs &A, int t, int lane, float *cs) {
   const double p = double(A.pos[t]);
   __syncwarp();
-  for (int j = lane; j < A.rot / 2; j += 32) {
-    double turns = p * A.inv_freq[j] * 0.15915494309189533577;   // 1 / (2 pi)
-    turns -= rint(turns);
-    float s, c;
-    sincospif(float(2.0 * turns), &s, &c);
-    cs[j] = c * A.rope_scale;
-    cs[kMaxD / 2 + j] = s * A.rope_scale;
+  for (int j = lane; j < 4 << A.lg; j += 32) {
+    float s = 0.f, c = 1.f;
+    if (j < A.rot / 2) {
+      double turns = p * A.inv_freq[j] * 0.15915494309189533577;   // 1 / (2 pi)
+      turns -= rint(turns);
+      sincospif(float(2.0 * turns), &s, &c);
+      c *= A.rope_scale;
+      s *= A.rope_scale;
+    }
+    cs[j] = c;
+    cs[kMaxD / 2 + j] = s;
   }
   __syncwarp();
 }
 
-// Element i (0..7) of the lane: its place in the row, and its factors: y = x c +
-// x' s for the turn by +angle (sign 1) or -angle.
+__device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+// Element i (0..7) of the lane: its place in the row.
 __device__ __forceinline__ int element(const Lane &L, int i) { return i < 4 ? L.a + i : L.b + i - 4; }
+
+// C and S for a turn by +angle (sign 1) or -angle, with the element's weight in
+// C and its partner's in S. w: a weight for each element.
 template <int PAIR>
-__device__ __forceinline__ void factors(const QkArgs &A, const Lane &L, const float *cs, int i, float sign,
-                                        float &c, float &s) {
-  c = 1.f;
-  s = 0.f;
-  const int e = element(L, i), half = A.rot / 2;
-  if (PAIR == kPairNone || e >= A.rot) return;
-  const bool first = PAIR == kPairInterleaved ? !(i & 1) : e < half;
-  const int j = PAIR == kPairInterleaved ? e / 2 : first ? e : e - half;
-  c = cs[j];
-  s = first ? -sign * cs[kMaxD / 2 + j] : sign * cs[kMaxD / 2 + j];
+__device__ __forceinline__ void factors(const QkArgs &A, const Lane &L, int l, const float *cs, const float *w,
+                                        float sign, Row &C, Row &S) {
+  const float4 wa = lds4(w + L.a), wb = lds4(w + L.b);
+  if (PAIR == kPairNone) {
+    C.v[0] = pair(wa.x, wa.y); C.v[1] = pair(wa.z, wa.w);
+    C.v[2] = pair(wb.x, wb.y); C.v[3] = pair(wb.z, wb.w);
+    return;
+  }
+  if (PAIR == kPairShared) {
+    float c[8], s[8];
+    const int half = A.rot / 2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = L.a + i, j = e < half ? e : e - half;
+      const bool on = e < A.rot;
+      c[i] = (on ? cs[j] : 1.f) * w[e];
+      s[i] = on ? sign * cs[kMaxD / 2 + j] * (e < half ? -w[e + half] : w[e - half]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      C.v[i] = pair(c[2 * i], c[2 * i + 1]);
+      S.v[i] = pair(s[2 * i], s[2 * i + 1]);
+    }
+    return;
+  }
+  const float4 c = lds4(cs + 4 * l);
+  float4 s = lds4(cs + kMaxD / 2 + 4 * l);
+  s = make_float4(s.x * sign, s.y * sign, s.z * sign, s.w * sign);
+  if (PAIR == kPairInterleaved) {
+    C.v[0] = pair(c.x * wa.x, c.x * wa.y); S.v[0] = pair(-s.x * wa.y, s.x * wa.x);
+    C.v[1] = pair(c.y * wa.z, c.y * wa.w); S.v[1] = pair(-s.y * wa.w, s.y * wa.z);
+    C.v[2] = pair(c.z * wb.x, c.z * wb.y); S.v[2] = pair(-s.z * wb.y, s.z * wb.x);
+    C.v[3] = pair(c.w * wb.z, c.w * wb.w); S.v[3] = pair(-s.w * wb.w, s.w * wb.z);
+  } else {
+    C.v[0] = pair(c.x * wa.x, c.y * wa.y); S.v[0] = pair(-s.x * wb.x, -s.y * wb.y);
+    C.v[1] = pair(c.z * wa.z, c.w * wa.w); S.v[1] = pair(-s.z * wb.z, -s.w * wb.w);
+    C.v[2] = pair(c.x * wb.x, c.y * wb.y); S.v[2] = pair(s.x * wa.x, s.y * wa.y);
+    C.v[3] = pair(c.z * wb.z, c.w * wb.w); S.v[3] = pair(s.z * wa.z, s.w * wa.w);
+  }
 }
 
 __device__ __forceinline__ float rnorm(const QkArgs &A, float ss) {
   return A.norm == GDN_NORM_NONE ? 1.f : rsqrtf(ss * A.inv_n + A.eps);
 }
 
-// w + w0 of the lane's elements, 1 without weights.
+// (w + w0) * scale of q's and of k's elements, 1 * scale without weights.
 template <typename T>
-__device__ __forceinline__ void load_w(const QkArgs &A, const Part &P, const Lane &L, float (&w)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    w[i] = 1.f;
-    const int e = element(L, i);
-    if (P.w && e < A.d) w[i] = to_f32(static_cast<const T *>(P.w)[e]) + A.w0;
+__device__ __forceinline__ void stage_weights(const QkArgs &A, bool scaled, bool weighted, float (*w)[kMaxD]) {
+  for (int i = threadIdx.x; i < 2 * kMaxD; i += kQkThreads) {
+    const Part &P = A.p[i / kMaxD];
+    const int e = i % kMaxD;
+    float x = 1.f;
+    if (weighted && P.w && e < A.d) x = to_f32(static_cast<const T *>(P.w)[e]) + A.w0;
+    w[i / kMaxD][e] = scaled ? x * P.scale : x;
   }
+  __syncthreads();
 }
 
-// Source of the rows: T in memory, or codes.
+// Source of the rows: T in memory, or codes. The pointers are those of the
+// lane's first row and step from row to row.
 template <typename T, bool PACKED, int PAIR, int ACC>
 struct Source {
-  Raw<T> raw;
-  __device__ __forceinline__ void load(const QkArgs &, const Part &P, int64_t t, int h, const Lane &L, bool on) {
-    load8<PAIR, ACC>(static_cast<const T *>(P.x) + t * P.x_ts + h * P.x_hs, L, on, raw);
+  using Data = Raw<T>;
+  const T *p;
+  int64_t step;
+  __device__ __forceinline__ Source(const QkArgs &, const Part &P, int64_t t, int h, int rows) {
+    p = static_cast<const T *>(P.x) + t * P.x_ts + h * P.x_hs;
+    step = rows * P.x_hs;
+  }
+  __device__ __forceinline__ void load(const Lane &L, bool on, Data &r) {
+    load8<PAIR, ACC>(p, L, on, r);
+    p += step;
   }
 };
 template <typename T, int PAIR, int ACC>
 struct Source<T, true, PAIR, ACC> {
-  Codes raw;
-  __device__ __forceinline__ void load(const QkArgs &A, const Part &P, int64_t t, int h, const Lane &L, bool on) {
+  using Data = Codes;
+  const uint8_t *p, *e;
+  int step, estep;
+  __device__ __forceinline__ Source(const QkArgs &A, const Part &P, int64_t t, int h, int rows) {
     const int64_t row = t * P.H + h;
-    const uint8_t *p = static_cast<const uint8_t *>(P.x) + row * A.d;
-    const uint8_t *e = P.x_scales + row * ((A.d + 31) / 32);
+    const int blocks = (A.d + 31) / 32;
+    p = static_cast<const uint8_t *>(P.x) + row * A.d;
+    e = P.x_scales + row * blocks;
+    step = rows * A.d;
+    estep = rows * blocks;
+  }
+  __device__ __forceinline__ void load(const Lane &L, bool on, Data &r) {
     if (ACC == 8 && PAIR != kPairSplit) {
-      raw.w[0] = raw.w[1] = 0;
-      raw.ea = 127;
+      r.w[0] = r.w[1] = 0;
+      r.ea = 127;
       if (on && L.na > 0) {
         const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p + L.a));
-        raw.w[0] = v.x; raw.w[1] = v.y;
-        raw.ea = e[L.a / 32];
+        r.w[0] = v.x; r.w[1] = v.y;
+        r.ea = e[L.a / 32];
       }
-      raw.eb = raw.ea;
+      r.eb = r.ea;
     } else {
-      raw.w[0] = load_codes<ACC>(p + L.a, on ? L.na : 0);
-      raw.w[1] = load_codes<ACC>(p + L.b, on ? L.nb : 0);
-      raw.ea = on && L.na > 0 ? e[L.a / 32] : 127;
-      raw.eb = on && L.nb > 0 ? e[L.b / 32] : 127;
+      r.w[0] = load_codes<ACC>(p + L.a, on ? L.na : 0);
+      r.w[1] = load_codes<ACC>(p + L.b, on ? L.nb : 0);
+      r.ea = on && L.na > 0 ? e[L.a / 32] : 127;
+      r.eb = on && L.nb > 0 ? e[L.b / 32] : 127;
     }
+    p += step;
+    e += estep;
   }
 };
 
-// The biased exponent that a block's largest finite magnitude asks for. 448 =
-// 1.75 * 2^8: its exponent - 8, and one more where the significand is above 1.75.
-__device__ __forceinline__ int block_exponent(float top) {
-  const uint32_t bits = __float_as_uint(top);
+// The biased exponent that a block's largest finite magnitude (its bits) asks
+// for. 448 = 1.75 * 2^8: its exponent - 8, one more where the significand is
+// above 1.75, and not below 2^-127.
+__device__ __forceinline__ int block_exponent(uint32_t bits) {
   return max(int((bits + 0x1fffffu) >> 23) - 8, 0);
-}
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a <= 3.402823466e38f ? a : 0.f;                // false for infinities and NaN
 }
 __device__ __forceinline__ uint32_t encode4(Pair lo, Pair hi, int be) {
   const float inv = __uint_as_float(uint32_t(254 - be) << 23);     // 2^-(be - 127)
@@ -377,61 +434,80 @@ __device__ __forceinline__ uint32_t encode4(Pair lo, Pair hi, int be) {
          uint32_t(__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3)) << 16;
 }
 
+// Largest magnitude of each chunk, as the upper 16 (bf16) or all (fp32) bits of
+// an fp32: of non-negative floats the bits compare alike, with infinities and
+// NaN above the rest. Two chunks' 16 bits share a word.
+struct Top { uint32_t a, b; };
+__device__ __forceinline__ Top chunk_tops(const Raw<__nv_bfloat16> &r) {
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t a = __vmaxu2(r.w[0] & m, r.w[1] & m), b = __vmaxu2(r.w[2] & m, r.w[3] & m);
+  const uint32_t t = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+  return {t << 16, t & 0xffff0000u};
+}
+__device__ __forceinline__ Top chunk_tops(const Raw<float> &r) {
+  uint32_t u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(r.w[i]) & 0x7fffffffu;
+  return {max(max(u[0], u[1]), max(u[2], u[3])), max(max(u[4], u[5]), max(u[6], u[7]))};
+}
+
 // Writes the lane's eight elements in 8 bits. Side by side, four lanes hold a
 // block; with halves in chunks eight lanes' first chunks do, and their second
 // chunks, where rot / 2 is a multiple of 32; for other rot the blocks' maxima
-// meet in shared memory (of non-negative floats the bits compare alike).
-template <int PAIR, int ACC>
+// meet in shared memory.
+template <typename T, int PAIR, int ACC>
 __device__ __forceinline__ void write_codes(const QkArgs &A, const Part &P, int64_t row, const Lane &L,
-                                            bool on, float *row_buf, const Row &x) {
-  float t[2];
-  bool fine = true;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float2 f = unpair(x.v[2 * i]), g = unpair(x.v[2 * i + 1]);
-    t[i] = fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(g.x), fabsf(g.y)));
-    fine &= f.x - f.x == 0.f && f.y - f.y == 0.f && g.x - g.x == 0.f && g.y - g.y == 0.f;
-  }
+                                            bool on, uint32_t *tops, const Raw<T> &raw, const Row &x) {
+  constexpr uint32_t kInf = 0x7f800000u;
+  Top t = chunk_tops(raw);
   Row z = x;
-  if (!fine) {                          // what is not finite counts for nothing, and becomes NaN
+  if (__any_sync(0xffffffffu, max(t.a, t.b) >= kInf)) {
+    // what is not finite counts for nothing, and becomes NaN
+    uint32_t u[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      t[i] = 0.f;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float2 f = unpair(x.v[2 * i + k]);
-        t[i] = fmaxf(t[i], fmaxf(finite_abs(f.x), finite_abs(f.y)));
-        if (f.x - f.x != 0.f) f.x = __int_as_float(0x7fffffff);
-        if (f.y - f.y != 0.f) f.y = __int_as_float(0x7fffffff);
-        z.v[2 * i + k] = pair(f.x, f.y);
-      }
+    for (int i = 0; i < 4; ++i) {
+      float2 f = unpair(x.v[i]);
+      const uint32_t fx = __float_as_uint(f.x) & 0x7fffffffu, fy = __float_as_uint(f.y) & 0x7fffffffu;
+      if (fx < kInf) u[i / 2] = max(u[i / 2], fx);
+      else f.x = __int_as_float(0x7fffffff);
+      if (fy < kInf) u[i / 2] = max(u[i / 2], fy);
+      else f.y = __int_as_float(0x7fffffff);
+      z.v[i] = pair(f.x, f.y);
     }
+    t = {u[0], u[1]};
   }
   const bool split = PAIR == kPairSplit && L.a < A.rot;
   if (PAIR == kPairSplit && A.rot % 64) {
-    uint32_t *top = reinterpret_cast<uint32_t *>(row_buf);
     __syncwarp();
-    if ((L.a & 31) == 0) top[L.a / 32] = 0;
-    if ((L.b & 31) == 0) top[L.b / 32] = 0;
+    if ((L.a & 31) == 0) tops[L.a / 32] = 0;
+    if ((L.b & 31) == 0) tops[L.b / 32] = 0;
     __syncwarp();
-    atomicMax(&top[L.a / 32], __float_as_uint(t[0]));
-    atomicMax(&top[L.b / 32], __float_as_uint(t[1]));
+    atomicMax(&tops[L.a / 32], t.a);
+    atomicMax(&tops[L.b / 32], t.b);
     __syncwarp();
-    t[0] = __uint_as_float(top[L.a / 32]);
-    t[1] = __uint_as_float(top[L.b / 32]);
+    t = {tops[L.a / 32], tops[L.b / 32]};
   } else {
-    if (!split) t[0] = t[1] = fmaxf(t[0], t[1]);
+    if (!split) t.a = t.b = max(t.a, t.b);
+    if (PAIR == kPairSplit && sizeof(T) == 2) {          // both chunks' 16 bits in one word
+      uint32_t w = __byte_perm(t.a, t.b, 0x7632);
+      w = __vmaxu2(w, __shfl_xor_sync(0xffffffffu, w, 1));
+      w = __vmaxu2(w, __shfl_xor_sync(0xffffffffu, w, 2));
+      const uint32_t o = __shfl_xor_sync(0xffffffffu, w, 4);
+      if (split) w = __vmaxu2(w, o);
+      t = {w << 16, w & 0xffff0000u};
+    } else {
 #pragma unroll
-    for (int off = 1; off < 4; off <<= 1) {
-      t[0] = fmaxf(t[0], __shfl_xor_sync(0xffffffffu, t[0], off));
-      if (PAIR == kPairSplit) t[1] = fmaxf(t[1], __shfl_xor_sync(0xffffffffu, t[1], off));
-    }
-    if (PAIR == kPairSplit) {
-      const float u0 = __shfl_xor_sync(0xffffffffu, t[0], 4), u1 = __shfl_xor_sync(0xffffffffu, t[1], 4);
-      if (split) { t[0] = fmaxf(t[0], u0); t[1] = fmaxf(t[1], u1); }
+      for (int off = 1; off < 8; off <<= 1) {
+        const uint32_t oa = __shfl_xor_sync(0xffffffffu, t.a, off);
+        if (off < 4 || split) t.a = max(t.a, oa);
+        if (PAIR == kPairSplit) {
+          const uint32_t ob = __shfl_xor_sync(0xffffffffu, t.b, off);
+          if (off < 4 || split) t.b = max(t.b, ob);
+        }
+      }
     }
   }
-  const int ea = block_exponent(t[0]), eb = PAIR == kPairSplit ? block_exponent(t[1]) : ea;
+  const int ea = block_exponent(t.a), eb = PAIR == kPairSplit ? block_exponent(t.b) : ea;
   const uint32_t ca = encode4(z.v[0], z.v[1], ea), cb = encode4(z.v[2], z.v[3], eb);
   if (!on) return;
   uint8_t *p = P.codes + row * A.d, *e = P.scales + row * ((A.d + 31) / 32);
@@ -449,7 +525,8 @@ __device__ __forceinline__ void write_codes(const QkArgs &A, const Part &P, int6
 struct Item { int t, r0, r1; };
 __device__ __forceinline__ Item item_at(const QkArgs &A, int64_t item) {
   Item I;
-  I.t = int(A.splits == 1 ? item : item / A.splits);
+  // tokens are shared out only where they are fewer than the warps
+  I.t = A.splits == 1 ? int(item) : int(unsigned(item) / unsigned(A.splits));
   I.r0 = int(item - int64_t(I.t) * A.splits) * A.rpi;
   I.r1 = min(A.p[0].H + A.p[1].H, I.r0 + A.rpi);
   return I;
@@ -459,14 +536,17 @@ __device__ __forceinline__ Item item_at(const QkArgs &A, int64_t item) {
 template <typename T, bool PACKED, bool PACK, int PAIR, int ACC>
 __global__ void __launch_bounds__(kQkThreads, 3) gdn_qk_fwd_kernel(const __grid_constant__ QkArgs A) {
   constexpr int U = 4;
-  __shared__ float cs_all[PAIR == kPairNone ? 1 : kQkWarps][kMaxD];
-  constexpr bool kRows = PAIR == kPairShared || (PACK && PAIR == kPairSplit);
-  __shared__ __align__(16) float rows_all[kRows ? kQkWarps : 1][kMaxD];
+  __shared__ __align__(16) float w_all[2][kMaxD];
+  __shared__ __align__(16) float cs_all[PAIR == kPairNone ? 1 : kQkWarps][kMaxD];
+  __shared__ __align__(16) float rows_all[PAIR == kPairShared ? kQkWarps : 1][kMaxD];
+  __shared__ uint32_t tops_all[PACK && PAIR == kPairSplit ? kQkWarps * 32 : 1];
   const int G = 1 << A.lg, R = 32 >> A.lg;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> A.lg;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> A.lg, l = lane & (G - 1);
   float *cs = cs_all[PAIR == kPairNone ? 0 : warp];
-  float *row_buf = rows_all[kRows ? warp : 0] + (lane & -G) * 8;
-  const Lane L = lane_place<PAIR>(A, lane & (G - 1));
+  float *row_buf = rows_all[PAIR == kPairShared ? warp : 0] + (lane & -G) * 8;
+  uint32_t *tops = tops_all + (PACK && PAIR == kPairSplit ? warp * 32 + sub * 8 : 0);
+  const Lane L = lane_place<PAIR>(A, l);
+  stage_weights<T>(A, true, true, w_all);
   const int64_t nwarps = int64_t(gridDim.x) * kQkWarps, items = int64_t(A.T) * A.splits;
   for (int64_t item = int64_t(blockIdx.x) * kQkWarps + warp; item < items; item += nwarps) {
     const Item I = item_at(A, item);
@@ -477,56 +557,32 @@ __global__ void __launch_bounds__(kQkThreads, 3) gdn_qk_fwd_kernel(const __grid_
       const int h0 = max(I.r0 - first, 0), h1 = min(I.r1 - first, P.H);
       if (h0 >= h1) continue;
       Row C, S;
-      {
-        float w[8];
-        load_w<T>(A, P, L, w);
+      factors<PAIR>(A, L, l, cs, w_all[part], 1.f, C, S);
+      using Src = Source<T, PACKED, PAIR, ACC>;
+      Src src(A, P, I.t, h0 + sub, R);
+      T *out = static_cast<T *>(P.out) + I.t * P.out_ts + (h0 + sub) * P.out_hs;
+      const int64_t out_step = R * P.out_hs;
+      for (int h = h0 + sub; h - sub < h1; h += R * U) {
+        typename Src::Data raw[U];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float c0, c1, s0, s1;
-          factors<PAIR>(A, L, cs, 2 * i, 1.f, c0, s0);
-          factors<PAIR>(A, L, cs, 2 * i + 1, 1.f, c1, s1);
-          C.v[i] = pair(c0 * w[2 * i] * P.scale, c1 * w[2 * i + 1] * P.scale);
-          S.v[i] = pair(s0 * P.scale, s1 * P.scale);
-        }
-        if (P.w && PAIR != kPairNone) {         // S takes the partner's weight
-          Row v, u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v.v[i] = pair(w[2 * i], w[2 * i + 1]);
-          partners<PAIR>(A, L, row_buf, v, u);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) S.v[i] = mul2(S.v[i], u.v[i]);
-        }
-      }
-      for (int h = h0; h < h1; h += R * U) {
-        Source<T, PACKED, PAIR, ACC> src[U];
+        for (int u = 0; u < U; ++u) src.load(L, h + u * R < h1, raw[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int hu = h + u * R + sub;
-          src[u].load(A, P, I.t, hu < h1 ? hu : h0, L, hu < h1);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (h + u * R >= h1) break;
-          const int hu = h + u * R + sub;
-          const bool on = hu < h1;
-          Row x, y;
-          unpack8(src[u].raw, x);
-          if (PACK && P.codes) write_codes<PAIR, ACC>(A, P, int64_t(I.t) * P.H + hu, L, on, row_buf, x);
-          if (PACK && !P.out) continue;
+          if (h - sub + u * R >= h1) break;
+          const bool on = h + u * R < h1;
+          Row x;
+          unpack8(raw[u], x);
+          if constexpr (PACK)
+            if (P.codes)
+              write_codes<T, PAIR, ACC>(A, P, int64_t(I.t) * P.H + h + u * R, L, on, tops, raw[u], x);
           if (A.norm != GDN_NORM_NONE) {
             const float r = rnorm(A, group_sum(dot8(x, x), A.lg));
 #pragma unroll
             for (int i = 0; i < 4; ++i) x.v[i] = mul2(x.v[i], pair(r, r));
           }
-          if (PAIR != kPairNone) {
-            partners<PAIR>(A, L, row_buf, x, y);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x.v[i] = fma2(y.v[i], S.v[i], mul2(x.v[i], C.v[i]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x.v[i] = mul2(x.v[i], C.v[i]);
-          }
-          if (on) store8<PAIR, ACC>(static_cast<T *>(P.out) + I.t * P.out_ts + hu * P.out_hs, L, x);
+          turn<PAIR>(A, L, row_buf, C, S, x);
+          if (on && (!PACK || P.out)) store8<PAIR, ACC>(out, L, x);
+          out += out_step;
         }
       }
     }
@@ -537,13 +593,16 @@ __global__ void __launch_bounds__(kQkThreads, 3) gdn_qk_fwd_kernel(const __grid_
 template <typename T, typename DT, bool PACKED, bool WEIGHTS, int PAIR, int ACC>
 __global__ void __launch_bounds__(kQkThreads, 2) gdn_qk_bwd_kernel(const __grid_constant__ QkArgs A) {
   constexpr int U = 2;
-  __shared__ float cs_all[PAIR == kPairNone ? 1 : kQkWarps][kMaxD];
+  __shared__ __align__(16) float w_all[2][kMaxD], one[2][kMaxD];
+  __shared__ __align__(16) float cs_all[PAIR == kPairNone ? 1 : kQkWarps][kMaxD];
   __shared__ __align__(16) float rows_all[PAIR == kPairShared || WEIGHTS ? kQkWarps : 1][kMaxD];
   const int G = 1 << A.lg, R = 32 >> A.lg;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> A.lg;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> A.lg, l = lane & (G - 1);
   float *cs = cs_all[PAIR == kPairNone ? 0 : warp];
   float *row_buf = rows_all[PAIR == kPairShared || WEIGHTS ? warp : 0] + (lane & -G) * 8;
-  const Lane L = lane_place<PAIR>(A, lane & (G - 1));
+  const Lane L = lane_place<PAIR>(A, l);
+  if (WEIGHTS) stage_weights<T>(A, false, true, w_all);
+  stage_weights<T>(A, true, false, one);
   const int64_t nwarps = int64_t(gridDim.x) * kQkWarps, items = int64_t(A.T) * A.splits;
   Row dw[2];
 #pragma unroll
@@ -558,46 +617,33 @@ __global__ void __launch_bounds__(kQkThreads, 2) gdn_qk_bwd_kernel(const __grid_
       const int h0 = max(I.r0 - first, 0), h1 = min(I.r1 - first, P.H);
       if (h0 >= h1) continue;
       Row C, S, W;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float c0, c1, s0, s1;
-        factors<PAIR>(A, L, cs, 2 * i, -1.f, c0, s0);
-        factors<PAIR>(A, L, cs, 2 * i + 1, -1.f, c1, s1);
-        C.v[i] = pair(c0 * P.scale, c1 * P.scale);
-        S.v[i] = pair(s0 * P.scale, s1 * P.scale);
-      }
+      factors<PAIR>(A, L, l, cs, one[part], -1.f, C, S);
       if (WEIGHTS) {
-        float w[8];
-        load_w<T>(A, P, L, w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) W.v[i] = pair(w[2 * i], w[2 * i + 1]);
+        const float4 wa = lds4(w_all[part] + L.a), wb = lds4(w_all[part] + L.b);
+        W.v[0] = pair(wa.x, wa.y); W.v[1] = pair(wa.z, wa.w);
+        W.v[2] = pair(wb.x, wb.y); W.v[3] = pair(wb.z, wb.w);
       }
-      for (int h = h0; h < h1; h += R * U) {
-        Source<T, PACKED, PAIR, ACC> src[U];
+      using Src = Source<T, PACKED, PAIR, ACC>;
+      Src src(A, P, I.t, h0 + sub, R);
+      const DT *dy = static_cast<const DT *>(P.dy) + I.t * P.dy_ts + (h0 + sub) * P.dy_hs;
+      T *out = static_cast<T *>(P.out) + I.t * P.out_ts + (h0 + sub) * P.out_hs;
+      const int64_t dy_step = R * P.dy_hs, out_step = R * P.out_hs;
+      for (int h = h0 + sub; h - sub < h1; h += R * U) {
+        typename Src::Data raw[U];
         Raw<DT> grad[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int hu = h + u * R + sub;
-          const bool on = hu < h1;
-          src[u].load(A, P, I.t, on ? hu : h0, L, on);
-          load8<PAIR, ACC>(static_cast<const DT *>(P.dy) + I.t * P.dy_ts + (on ? hu : h0) * P.dy_hs, L, on,
-                           grad[u]);
+          src.load(L, h + u * R < h1, raw[u]);
+          load8<PAIR, ACC>(dy, L, h + u * R < h1, grad[u]);
+          dy += dy_step;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (h + u * R >= h1) break;
-          const int hu = h + u * R + sub;
-          Row x, z, y;
-          unpack8(src[u].raw, x);
+          if (h - sub + u * R >= h1) break;
+          Row x, z;
+          unpack8(raw[u], x);
           unpack8(grad[u], z);
-          if (PAIR != kPairNone) {
-            partners<PAIR>(A, L, row_buf, z, y);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z.v[i] = fma2(y.v[i], S.v[i], mul2(z.v[i], C.v[i]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z.v[i] = mul2(z.v[i], C.v[i]);
-          }
+          turn<PAIR>(A, L, row_buf, C, S, z);
           float r = 1.f, m = 0.f;
           Row dh = z;
           if (WEIGHTS) {
@@ -615,7 +661,8 @@ __global__ void __launch_bounds__(kQkThreads, 2) gdn_qk_bwd_kernel(const __grid_
             if (WEIGHTS) dw[part].v[i] = fma2(z.v[i], hx, dw[part].v[i]);
             x.v[i] = A.norm == GDN_NORM_NONE ? dh.v[i] : mul2(fma2(hx, mm, dh.v[i]), rr);
           }
-          if (hu < h1) store8<PAIR, ACC>(static_cast<T *>(P.out) + I.t * P.out_ts + hu * P.out_hs, L, x);
+          if (h + u * R < h1) store8<PAIR, ACC>(out, L, x);
+          out += out_step;
         }
       }
     }
