@@ -11,15 +11,16 @@
 //   dh = (w + w0) dz,   dx = r (dh - h (dh . h) / n)
 // A row is read once and written once: the kernels are bound by HBM.
 //
-// A group of G lanes (8, 16 or 32: from d / 8 up) holds a row, eight elements
-// a lane in two chunks of four, so the sums are log2 G shuffles. For pairs of
-// halves the chunks lie rot / 2 apart (rot a multiple of 8), otherwise side by
-// side: a pair's two elements are in one lane either way and nothing is
-// exchanged. Only halves that do not fall into chunks of four (odd rot, rows
-// off their alignment) meet in the warp's own shared memory. With
-// y = r (x C + x' S), x' the partner's element, C and S hold cosine, sine,
-// weight and scale, formed once for all heads of q and of k of a token, and the
-// row's arithmetic is 12 paired instructions for 8 elements.
+// A group of G lanes holds a row, two chunks of E elements a lane (E = 8 in the
+// forward kernels, 4 in the backward ones, which hold more a row), so the sums
+// are log2 G shuffles. For pairs of halves the chunks lie rot / 2 apart (rot a
+// multiple of 2 E), otherwise side by side: a pair's two elements are in one
+// lane either way and nothing is exchanged. Only halves that do not fall into
+// chunks (odd rot, rows off their alignment) meet in the warp's own shared
+// memory. With y = r (x C + x' S), x' the partner's element, C and S hold
+// cosine, sine, weight and scale, formed once for all heads of q and of k of a
+// token, and a row's arithmetic is two or three paired instructions an element
+// pair and part of the sum.
 //
 // A warp takes an item: rows of one token, q's heads and then k's. It forms the
 // item's cosines and sines once: the angle in turns is position * inv_freq /
@@ -41,6 +42,7 @@ namespace {
 
 constexpr int kQkThreads = 256, kQkWarps = kQkThreads / 32;
 constexpr int kMaxD = 256;
+constexpr int kFwdBlocksPerSm = 2, kBwdBlocksPerSm = 2;
 
 // How the pairs lie. Split: halves in chunks of four; shared: any halves.
 enum { kPairNone, kPairInterleaved, kPairSplit, kPairShared };
@@ -52,7 +54,8 @@ struct Part {                     // q or k
   void *out;                      // y or dx; may be null when only codes are wanted
   uint8_t *codes, *scales;        // checkpoint to write, or null
   const void *w;
-  int64_t x_ts, x_hs, dy_ts, dy_hs, out_ts, out_hs;
+  int64_t x_ts, dy_ts, out_ts;    // bytes between tokens
+  int x_hs, dy_hs, out_hs;        // bytes between heads
   int H;                          // heads
   float scale;
 };
@@ -68,107 +71,124 @@ struct QkArgs {
   float eps, w0, rope_scale, inv_n;
 };
 
-// A lane's place in a row: chunks of four elements at a and b, of which na and
-// nb exist.
+// A lane's place in a row: chunks of E elements at a and b, of which na and nb
+// exist.
 struct Lane { int a, b, na, nb; };
-template <int PAIR>
+template <int E, int PAIR>
 __device__ __forceinline__ Lane lane_place(const QkArgs &A, int l) {
   Lane L;
-  const bool split = PAIR == kPairSplit && 8 * l < A.rot;
-  L.a = split ? 4 * l : 8 * l;
-  L.b = split ? A.rot / 2 + 4 * l : 8 * l + 4;
-  L.na = max(0, min(4, A.d - L.a));
-  L.nb = max(0, min(4, A.d - L.b));
+  const bool split = PAIR == kPairSplit && 2 * E * l < A.rot;
+  L.a = split ? E * l : 2 * E * l;
+  L.b = split ? A.rot / 2 + E * l : 2 * E * l + E;
+  L.na = max(0, min(E, A.d - L.a));
+  L.nb = max(0, min(E, A.d - L.b));
   return L;
 }
 
-// Eight elements as they lie in memory.
-template <typename T>
+// Two chunks as they lie in memory.
+template <typename T, int E>
 struct Raw;
-template <>
-struct Raw<__nv_bfloat16> { uint32_t w[4]; };
-template <>
-struct Raw<float> { float w[8]; };
-struct Codes { uint32_t w[2]; uint32_t ea, eb; };
+template <int E>
+struct Raw<__nv_bfloat16, E> { uint32_t w[E]; };
+template <int E>
+struct Raw<float, E> { float w[2 * E]; };
+template <int E>
+struct Codes { uint32_t w[E / 2]; uint32_t ea, eb; };
 
-// ACC: elements an access may take; all pointers and strides are multiples of it.
-template <int ACC>
+// ACC: elements an access may take; all pointers and strides are multiples of
+// it. Where a chunk is one access or several whole ones (ACC >= E) it exists or
+// not as a whole: it is then read without a condition, what does not exist from
+// the row's beginning, and left out of the sums. Otherwise n elements are read
+// and the rest is zero.
+template <int E, int ACC>
 __device__ __forceinline__ void load_chunk(const __nv_bfloat16 *p, int n, uint32_t *w) {
-  w[0] = w[1] = 0;
-  if (ACC >= 4) {
-    if (n > 0) {
-      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
-      w[0] = v.x; w[1] = v.y;
-    }
+  if (ACC >= E && E == 8) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else if (ACC >= E) {
+    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+    w[0] = v.x; w[1] = v.y;
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) w[i / 2] |= uint32_t(*reinterpret_cast<const uint16_t *>(p + i)) << (16 * (i & 1));
+    for (int i = 0; i < E / 2; ++i) w[i] = 0;
+    if (ACC == 4) {
+#pragma unroll
+      for (int i = 0; i < E; i += 4)
+        if (i < n) {
+          const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p + i));
+          w[i / 2] = v.x; w[i / 2 + 1] = v.y;
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (i < n) w[i / 2] |= uint32_t(*reinterpret_cast<const uint16_t *>(p + i)) << (16 * (i & 1));
+    }
   }
 }
-template <int ACC>
+template <int E, int ACC>
 __device__ __forceinline__ void load_chunk(const float *p, int n, float *w) {
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (ACC >= 4) {
-    if (n > 0) v = __ldcs(reinterpret_cast<const float4 *>(p));
-  } else {
-    if (n > 0) v.x = p[0];
-    if (n > 1) v.y = p[1];
-    if (n > 2) v.z = p[2];
-    if (n > 3) v.w = p[3];
-  }
-  w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-}
-template <int PAIR, int ACC>
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, const Lane &L, bool on, Raw<__nv_bfloat16> &r) {
-  if (ACC == 8 && PAIR != kPairSplit) {
-    r.w[0] = r.w[1] = r.w[2] = r.w[3] = 0;
-    if (on && L.na > 0) {
-      const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p + L.a));
-      r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+#pragma unroll
+  for (int i = 0; i < E; i += 4) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (ACC >= E) {
+      v = __ldcs(reinterpret_cast<const float4 *>(p + i));
+    } else if (ACC == 4) {
+      if (i < n) v = __ldcs(reinterpret_cast<const float4 *>(p + i));
+    } else {
+      if (i + 0 < n) v.x = p[i];
+      if (i + 1 < n) v.y = p[i + 1];
+      if (i + 2 < n) v.z = p[i + 2];
+      if (i + 3 < n) v.w = p[i + 3];
     }
-  } else {
-    load_chunk<ACC>(p + L.a, on ? L.na : 0, r.w);
-    load_chunk<ACC>(p + L.b, on ? L.nb : 0, r.w + 2);
+    w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
   }
 }
-template <int PAIR, int ACC>
-__device__ __forceinline__ void load8(const float *p, const Lane &L, bool on, Raw<float> &r) {
-  load_chunk<ACC>(p + L.a, on ? L.na : 0, r.w);
-  load_chunk<ACC>(p + L.b, on ? L.nb : 0, r.w + 4);
-}
-template <int ACC>
-__device__ __forceinline__ uint32_t load_codes(const uint8_t *p, int n) {
-  uint32_t w = 0;
-  if (ACC >= 4) {
-    if (n > 0) w = __ldcs(reinterpret_cast<const uint32_t *>(p));
+template <int E, int ACC>
+__device__ __forceinline__ void load_chunk(const uint8_t *p, int n, uint32_t *w) {
+  if (ACC >= E && E == 8) {
+    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+    w[0] = v.x; w[1] = v.y;
+  } else if (ACC >= E) {
+    w[0] = __ldcs(reinterpret_cast<const uint32_t *>(p));
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) w |= uint32_t(p[i]) << (8 * i);
+    for (int i = 0; i < E; i += 4) {
+      w[i / 4] = 0;
+      if (ACC == 4) {
+        if (i < n) w[i / 4] = __ldcs(reinterpret_cast<const uint32_t *>(p + i));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (i + k < n) w[i / 4] |= uint32_t(p[i + k]) << (8 * k);
+      }
+    }
   }
-  return w;
 }
 
-// The lane's elements as four pairs: chunk a, then chunk b.
-struct Row { Pair v[4]; };
+// The lane's elements as E pairs: chunk a, then chunk b.
+template <int E>
+struct Row { Pair v[E]; };
 
-__device__ __forceinline__ void unpack8(const Raw<__nv_bfloat16> &r, Row &x) {
+template <int E>
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16, E> &r, Row<E> &x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x.v[i] = pair(bf_lo(r.w[i]), bf_hi(r.w[i]));
+  for (int i = 0; i < E; ++i) x.v[i] = pair(bf_lo(r.w[i]), bf_hi(r.w[i]));
 }
-__device__ __forceinline__ void unpack8(const Raw<float> &r, Row &x) {
+template <int E>
+__device__ __forceinline__ void unpack(const Raw<float, E> &r, Row<E> &x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x.v[i] = pair(r.w[2 * i], r.w[2 * i + 1]);
+  for (int i = 0; i < E; ++i) x.v[i] = pair(r.w[2 * i], r.w[2 * i + 1]);
 }
 // 2^(b - 127), b in [0, 254]: 2^-127 lies below the normal range.
 __device__ __forceinline__ float pow2_biased(uint32_t b) {
   return __uint_as_float(b ? b << 23 : 0x00400000u);
 }
-__device__ __forceinline__ void unpack8(const Codes &r, Row &x) {
+template <int E>
+__device__ __forceinline__ void unpack(const Codes<E> &r, Row<E> &x) {
+  const float sa = pow2_biased(r.ea), sb = pow2_biased(r.eb);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float s = pow2_biased(i < 2 ? r.ea : r.eb);
+  for (int i = 0; i < E; ++i) {
+    const float s = i < E / 2 ? sa : sb;
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
         static_cast<__nv_fp8x2_storage_t>((r.w[i / 2] >> (16 * (i & 1))) & 0xffff), __NV_E4M3);
     const float2 f = __half22float2(__half2(h));
@@ -176,58 +196,85 @@ __device__ __forceinline__ void unpack8(const Codes &r, Row &x) {
   }
 }
 
-template <int ACC>
-__device__ __forceinline__ void store_chunk(__nv_bfloat16 *p, int n, Pair lo, Pair hi) {
-  const float2 f = unpair(lo), g = unpair(hi);
-  const uint32_t w[2] = {bf_pack(f.x, f.y), bf_pack(g.x, g.y)};
-  if (ACC >= 4) {
-    if (n > 0) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+template <int E, int ACC>
+__device__ __forceinline__ void store_chunk(__nv_bfloat16 *p, int n, const Pair *v) {
+  uint32_t w[E / 2];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    const float2 f = unpair(v[i]);
+    w[i] = bf_pack(f.x, f.y);
+  }
+  if (ACC >= E && E == 8) {
+    if (n > 0) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if (ACC >= 4) {
+#pragma unroll
+    for (int i = 0; i < E; i += 4)
+      if (i < n) *reinterpret_cast<uint2 *>(p + i) = make_uint2(w[i / 2], w[i / 2 + 1]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < E; ++i)
       if (i < n) *reinterpret_cast<uint16_t *>(p + i) = uint16_t(w[i / 2] >> (16 * (i & 1)));
   }
 }
-template <int ACC>
-__device__ __forceinline__ void store_chunk(float *p, int n, Pair lo, Pair hi) {
-  const float2 f = unpair(lo), g = unpair(hi);
-  if (ACC >= 4) {
-    if (n > 0) *reinterpret_cast<float4 *>(p) = make_float4(f.x, f.y, g.x, g.y);
-  } else {
-    if (n > 0) p[0] = f.x;
-    if (n > 1) p[1] = f.y;
-    if (n > 2) p[2] = g.x;
-    if (n > 3) p[3] = g.y;
-  }
-}
-template <int PAIR, int ACC>
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const Lane &L, const Row &y) {
-  if (ACC == 8 && PAIR != kPairSplit) {
-    uint32_t w[4];
+template <int E, int ACC>
+__device__ __forceinline__ void store_chunk(float *p, int n, const Pair *v) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpair(y.v[i]);
-      w[i] = bf_pack(f.x, f.y);
+  for (int i = 0; i < E; i += 4) {
+    const float2 f = unpair(v[i / 2]), g = unpair(v[i / 2 + 1]);
+    if (ACC >= 4) {
+      if (i < n) *reinterpret_cast<float4 *>(p + i) = make_float4(f.x, f.y, g.x, g.y);
+    } else {
+      if (i + 0 < n) p[i] = f.x;
+      if (i + 1 < n) p[i + 1] = f.y;
+      if (i + 2 < n) p[i + 2] = g.x;
+      if (i + 3 < n) p[i + 3] = g.y;
     }
-    if (L.na > 0) *reinterpret_cast<uint4 *>(p + L.a) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    store_chunk<ACC>(p + L.a, L.na, y.v[0], y.v[1]);
-    store_chunk<ACC>(p + L.b, L.nb, y.v[2], y.v[3]);
   }
 }
-template <int PAIR, int ACC>
-__device__ __forceinline__ void store8(float *p, const Lane &L, const Row &y) {
-  store_chunk<ACC>(p + L.a, L.na, y.v[0], y.v[1]);
-  store_chunk<ACC>(p + L.b, L.nb, y.v[2], y.v[3]);
-}
-template <int ACC>
-__device__ __forceinline__ void store_codes(uint8_t *p, int n, uint32_t w) {
-  if (ACC >= 4) {
-    if (n > 0) *reinterpret_cast<uint32_t *>(p) = w;
+template <int E, int ACC>
+__device__ __forceinline__ void store_codes(uint8_t *p, int n, const uint32_t *w) {
+  if (ACC >= E && E == 8) {
+    if (n > 0) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+  } else if (ACC >= 4) {
+#pragma unroll
+    for (int i = 0; i < E; i += 4)
+      if (i < n) *reinterpret_cast<uint32_t *>(p + i) = w[i / 4];
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) p[i] = uint8_t(w >> (8 * i));
+    for (int i = 0; i < E; ++i)
+      if (i < n) p[i] = uint8_t(w[i / 4] >> (8 * (i & 3)));
+  }
+}
+
+// Heads' rows of one token, at the lane's chunks: one multiply-add an address.
+template <typename P>
+struct Rows {
+  P *a, *b;
+  int hs;
+  __device__ __forceinline__ Rows(P *p, int64_t offset, int head_stride, const Lane &L, bool reads) {
+    char *q = const_cast<char *>(reinterpret_cast<const char *>(p)) + offset;
+    // chunks that do not exist are read at the row's beginning
+    a = reinterpret_cast<P *>(q) + (reads && L.na == 0 ? 0 : L.a);
+    b = reinterpret_cast<P *>(q) + (reads && L.nb == 0 ? 0 : L.b);
+    hs = head_stride;
+  }
+  static __device__ __forceinline__ P *at(P *p, int h, int hs) {
+    return reinterpret_cast<P *>(const_cast<char *>(reinterpret_cast<const char *>(p)) + int64_t(h) * hs);
+  }
+  __device__ __forceinline__ P *first(int h) const { return at(a, h, hs); }
+  __device__ __forceinline__ P *second(int h) const { return at(b, h, hs); }
+};
+template <int E, int ACC, typename T>
+__device__ __forceinline__ void load_row(const Rows<const T> &P, int h, const Lane &L, Raw<T, E> &r) {
+  constexpr int half = sizeof(r.w) / sizeof(r.w[0]) / 2;
+  if (ACC == 8 && E == 4 && sizeof(T) == 2) {        // side by side (see with_variant)
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(P.first(h)));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 2 * half; ++i) reinterpret_cast<uint32_t &>(r.w[i]) = w[i & 3];
+  } else {
+    load_chunk<E, ACC>(P.first(h), L.na, r.w);
+    load_chunk<E, ACC>(P.second(h), L.nb, r.w + half);
   }
 }
 
@@ -235,47 +282,58 @@ __device__ __forceinline__ void store_codes(uint8_t *p, int n, uint32_t w) {
 __device__ __forceinline__ float group_sum(float x, int lg) {
   if (lg > 4) x += __shfl_xor_sync(0xffffffffu, x, 16);
   if (lg > 3) x += __shfl_xor_sync(0xffffffffu, x, 8);
-#pragma unroll
-  for (int off = 4; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  if (lg > 2) x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 2);
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
   return x;
 }
-__device__ __forceinline__ float dot8(const Row &x, const Row &y) {
-  Pair s = mul2(x.v[0], y.v[0]);
+// x . y over the lane's elements; chunks that do not exist count for nothing.
+template <int E, bool WHOLE>
+__device__ __forceinline__ float dot(const Lane &L, const Row<E> &x, const Row<E> &y) {
+  Pair s = mul2(x.v[0], y.v[0]), t = mul2(x.v[E / 2], y.v[E / 2]);
 #pragma unroll
-  for (int i = 1; i < 4; ++i) s = fma2(x.v[i], y.v[i], s);
-  const float2 f = unpair(s);
-  return f.x + f.y;
+  for (int i = 1; i < E / 2; ++i) {
+    s = fma2(x.v[i], y.v[i], s);
+    t = fma2(x.v[E / 2 + i], y.v[E / 2 + i], t);
+  }
+  const float2 f = unpair(s), g = unpair(t);
+  float a = f.x + f.y, b = g.x + g.y;
+  if (WHOLE) {
+    a = L.na > 0 ? a : 0.f;
+    b = L.nb > 0 ? b : 0.f;
+  }
+  return a + b;
 }
 
-// The lane's part of y = x C + x' S, x' the partner of every element. What does
+// The lane's part of x C + x' S, x' the partner of every element. What does
 // not turn takes no partner: it must not meet another element's infinity.
 // row: this group's part of the warp's buffer.
-template <int PAIR>
-__device__ __forceinline__ void turn(const QkArgs &A, const Lane &L, float *row, const Row &C, const Row &S,
-                                     Row &x) {
-  Row y;
+template <int E, int PAIR>
+__device__ __forceinline__ void turn(const QkArgs &A, const Lane &L, float *row, const Row<E> &C,
+                                     const Row<E> &S, Row<E> &x) {
+  Row<E> y;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) y.v[i] = mul2(x.v[i], C.v[i]);
+  for (int i = 0; i < E; ++i) y.v[i] = mul2(x.v[i], C.v[i]);
   if (PAIR == kPairInterleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < E; ++i) {
       const float2 f = unpair(x.v[i]);
       if (L.a + 2 * i < A.rot) y.v[i] = fma2(pair(f.y, f.x), S.v[i], y.v[i]);
     }
   } else if (PAIR == kPairSplit) {
     if (L.a < A.rot) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y.v[i] = fma2(x.v[i ^ 2], S.v[i], y.v[i]);
+      for (int i = 0; i < E; ++i) y.v[i] = fma2(x.v[i ^ (E / 2)], S.v[i], y.v[i]);
     }
   } else if (PAIR == kPairShared) {
     const int half = A.rot / 2;
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < E; ++i)
       *reinterpret_cast<float2 *>(row + L.a + 2 * i) = unpair(x.v[i]);
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < E; ++i) {
       float2 f;
       const int e = L.a + 2 * i, g = e + 1;
       f.x = e < A.rot ? row[e < half ? e + half : e - half] : 0.f;
@@ -288,10 +346,10 @@ __device__ __forceinline__ void turn(const QkArgs &A, const Lane &L, float *row,
 
 // The item's cosines and sines, in the warp's buffer: cs[j], cs[kMaxD / 2 + j];
 // 1 and 0 for the pairs that do not turn.
-__device__ __forceinline__ void make_angles(const QkArgs &A, int t, int lane, float *cs) {
+__device__ __forceinline__ void make_angles(const QkArgs &A, int t, int lane, int pairs, float *cs) {
   const double p = double(A.pos[t]);
   __syncwarp();
-  for (int j = lane; j < 4 << A.lg; j += 32) {
+  for (int j = lane; j < pairs; j += 32) {
     float s = 0.f, c = 1.f;
     if (j < A.rot / 2) {
       double turns = p * A.inv_freq[j] * 0.15915494309189533577;   // 1 / (2 pi)
@@ -307,50 +365,54 @@ __device__ __forceinline__ void make_angles(const QkArgs &A, int t, int lane, fl
 }
 
 __device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-// Element i (0..7) of the lane: its place in the row.
-__device__ __forceinline__ int element(const Lane &L, int i) { return i < 4 ? L.a + i : L.b + i - 4; }
+template <int E>
+__device__ __forceinline__ void lds(const float *p, float *x) {
+#pragma unroll
+  for (int i = 0; i < E; i += 4) {
+    const float4 v = lds4(p + i);
+    x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+  }
+}
 
 // C and S for a turn by +angle (sign 1) or -angle, with the element's weight in
 // C and its partner's in S. w: a weight for each element.
-template <int PAIR>
+template <int E, int PAIR>
 __device__ __forceinline__ void factors(const QkArgs &A, const Lane &L, int l, const float *cs, const float *w,
-                                        float sign, Row &C, Row &S) {
-  const float4 wa = lds4(w + L.a), wb = lds4(w + L.b);
+                                        float sign, Row<E> &C, Row<E> &S) {
+  float wa[2 * E];
+  lds<E>(w + L.a, wa);
+  lds<E>(w + L.b, wa + E);
+  float c[2 * E], s[2 * E];
   if (PAIR == kPairNone) {
-    C.v[0] = pair(wa.x, wa.y); C.v[1] = pair(wa.z, wa.w);
-    C.v[2] = pair(wb.x, wb.y); C.v[3] = pair(wb.z, wb.w);
-    return;
-  }
-  if (PAIR == kPairShared) {
-    float c[8], s[8];
+#pragma unroll
+    for (int i = 0; i < 2 * E; ++i) c[i] = wa[i], s[i] = 0.f;
+  } else if (PAIR == kPairShared) {
     const int half = A.rot / 2;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 2 * E; ++i) {
       const int e = L.a + i, j = e < half ? e : e - half;
       const bool on = e < A.rot;
-      c[i] = (on ? cs[j] : 1.f) * w[e];
+      c[i] = (on ? cs[j] : 1.f) * wa[i];
       s[i] = on ? sign * cs[kMaxD / 2 + j] * (e < half ? -w[e + half] : w[e - half]) : 0.f;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      C.v[i] = pair(c[2 * i], c[2 * i + 1]);
-      S.v[i] = pair(s[2 * i], s[2 * i + 1]);
-    }
-    return;
-  }
-  const float4 c = lds4(cs + 4 * l);
-  float4 s = lds4(cs + kMaxD / 2 + 4 * l);
-  s = make_float4(s.x * sign, s.y * sign, s.z * sign, s.w * sign);
-  if (PAIR == kPairInterleaved) {
-    C.v[0] = pair(c.x * wa.x, c.x * wa.y); S.v[0] = pair(-s.x * wa.y, s.x * wa.x);
-    C.v[1] = pair(c.y * wa.z, c.y * wa.w); S.v[1] = pair(-s.y * wa.w, s.y * wa.z);
-    C.v[2] = pair(c.z * wb.x, c.z * wb.y); S.v[2] = pair(-s.z * wb.y, s.z * wb.x);
-    C.v[3] = pair(c.w * wb.z, c.w * wb.w); S.v[3] = pair(-s.w * wb.w, s.w * wb.z);
   } else {
-    C.v[0] = pair(c.x * wa.x, c.y * wa.y); S.v[0] = pair(-s.x * wb.x, -s.y * wb.y);
-    C.v[1] = pair(c.z * wa.z, c.w * wa.w); S.v[1] = pair(-s.z * wb.z, -s.w * wb.w);
-    C.v[2] = pair(c.x * wb.x, c.y * wb.y); S.v[2] = pair(s.x * wa.x, s.y * wa.y);
-    C.v[3] = pair(c.z * wb.z, c.w * wb.w); S.v[3] = pair(s.z * wa.z, s.w * wa.w);
+    float cj[E], sj[E];
+    lds<E>(cs + E * l, cj);
+    lds<E>(cs + kMaxD / 2 + E * l, sj);
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      // the pair's elements: neighbours, or one of each chunk
+      const int i = PAIR == kPairInterleaved ? 2 * j : j, k = PAIR == kPairInterleaved ? 2 * j + 1 : j + E;
+      c[i] = cj[j] * wa[i];
+      c[k] = cj[j] * wa[k];
+      s[i] = -sign * sj[j] * wa[k];
+      s[k] = sign * sj[j] * wa[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    C.v[i] = pair(c[2 * i], c[2 * i + 1]);
+    S.v[i] = pair(s[2 * i], s[2 * i + 1]);
   }
 }
 
@@ -371,53 +433,36 @@ __device__ __forceinline__ void stage_weights(const QkArgs &A, bool scaled, bool
   __syncthreads();
 }
 
-// Source of the rows: T in memory, or codes. The pointers are those of the
-// lane's first row and step from row to row.
-template <typename T, bool PACKED, int PAIR, int ACC>
+// Source of the rows: T in memory, or codes.
+template <typename T, bool PACKED, int E, int PAIR, int ACC>
 struct Source {
-  using Data = Raw<T>;
-  const T *p;
-  int64_t step;
-  __device__ __forceinline__ Source(const QkArgs &, const Part &P, int64_t t, int h, int rows) {
-    p = static_cast<const T *>(P.x) + t * P.x_ts + h * P.x_hs;
-    step = rows * P.x_hs;
-  }
-  __device__ __forceinline__ void load(const Lane &L, bool on, Data &r) {
-    load8<PAIR, ACC>(p, L, on, r);
-    p += step;
+  using Data = Raw<T, E>;
+  Rows<const T> rows;
+  __device__ __forceinline__ Source(const QkArgs &, const Part &P, int64_t t, const Lane &L)
+      : rows(static_cast<const T *>(P.x), t * P.x_ts, P.x_hs, L, true) {}
+  __device__ __forceinline__ void load(int h, const Lane &L, Data &r) const {
+    load_row<E, ACC>(rows, h, L, r);
   }
 };
-template <typename T, int PAIR, int ACC>
-struct Source<T, true, PAIR, ACC> {
-  using Data = Codes;
-  const uint8_t *p, *e;
-  int step, estep;
-  __device__ __forceinline__ Source(const QkArgs &A, const Part &P, int64_t t, int h, int rows) {
-    const int64_t row = t * P.H + h;
-    const int blocks = (A.d + 31) / 32;
-    p = static_cast<const uint8_t *>(P.x) + row * A.d;
-    e = P.x_scales + row * blocks;
-    step = rows * A.d;
-    estep = rows * blocks;
+template <typename T, int E, int PAIR, int ACC>
+struct Source<T, true, E, PAIR, ACC> {
+  using Data = Codes<E>;
+  Rows<const uint8_t> rows;
+  const uint8_t *e;
+  int blocks, ea, eb;
+  __device__ __forceinline__ Source(const QkArgs &A, const Part &P, int64_t t, const Lane &L)
+      : rows(static_cast<const uint8_t *>(P.x), t * P.H * A.d, A.d, L, true) {
+    blocks = (A.d + 31) / 32;
+    e = P.x_scales + t * P.H * blocks;
+    ea = L.na > 0 ? L.a / 32 : 0;
+    eb = L.nb > 0 ? L.b / 32 : 0;
   }
-  __device__ __forceinline__ void load(const Lane &L, bool on, Data &r) {
-    if (ACC == 8 && PAIR != kPairSplit) {
-      r.w[0] = r.w[1] = 0;
-      r.ea = 127;
-      if (on && L.na > 0) {
-        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p + L.a));
-        r.w[0] = v.x; r.w[1] = v.y;
-        r.ea = e[L.a / 32];
-      }
-      r.eb = r.ea;
-    } else {
-      r.w[0] = load_codes<ACC>(p + L.a, on ? L.na : 0);
-      r.w[1] = load_codes<ACC>(p + L.b, on ? L.nb : 0);
-      r.ea = on && L.na > 0 ? e[L.a / 32] : 127;
-      r.eb = on && L.nb > 0 ? e[L.b / 32] : 127;
-    }
-    p += step;
-    e += estep;
+  __device__ __forceinline__ void load(int h, const Lane &L, Data &r) const {
+    load_chunk<E, ACC>(rows.first(h), L.na, r.w);
+    load_chunk<E, ACC>(rows.second(h), L.nb, r.w + E / 4);
+    const uint8_t *s = e + int64_t(h) * blocks;
+    r.ea = s[ea];
+    r.eb = PAIR == kPairSplit ? s[eb] : r.ea;        // side by side, both are of one block
   }
 };
 
@@ -427,54 +472,69 @@ struct Source<T, true, PAIR, ACC> {
 __device__ __forceinline__ int block_exponent(uint32_t bits) {
   return max(int((bits + 0x1fffffu) >> 23) - 8, 0);
 }
-__device__ __forceinline__ uint32_t encode4(Pair lo, Pair hi, int be) {
-  const float inv = __uint_as_float(uint32_t(254 - be) << 23);     // 2^-(be - 127)
-  const float2 a = unpair(mul2(lo, pair(inv, inv))), b = unpair(mul2(hi, pair(inv, inv)));
-  return __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
-         uint32_t(__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3)) << 16;
-}
-
-// Largest magnitude of each chunk, as the upper 16 (bf16) or all (fp32) bits of
-// an fp32: of non-negative floats the bits compare alike, with infinities and
-// NaN above the rest. Two chunks' 16 bits share a word.
+// Largest magnitude of each chunk, as bits of an fp32: of non-negative floats
+// the bits compare alike, with infinities and NaN above the rest. bf16 compares
+// two at a time in 16 bits.
 struct Top { uint32_t a, b; };
-__device__ __forceinline__ Top chunk_tops(const Raw<__nv_bfloat16> &r) {
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <int E>
+__device__ __forceinline__ Top chunk_tops(const Raw<__nv_bfloat16, E> &r) {
   const uint32_t m = 0x7fff7fffu;
-  const uint32_t a = __vmaxu2(r.w[0] & m, r.w[1] & m), b = __vmaxu2(r.w[2] & m, r.w[3] & m);
-  const uint32_t t = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+  uint32_t a = r.w[0] & m, b = r.w[E / 2] & m;
+#pragma unroll
+  for (int i = 1; i < E / 2; ++i) {
+    a = max16x2(a, r.w[i] & m);
+    b = max16x2(b, r.w[E / 2 + i] & m);
+  }
+  const uint32_t t = max16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
   return {t << 16, t & 0xffff0000u};
 }
-__device__ __forceinline__ Top chunk_tops(const Raw<float> &r) {
-  uint32_t u[8];
+template <int E>
+__device__ __forceinline__ Top chunk_tops(const Raw<float, E> &r) {
+  Top t = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(r.w[i]) & 0x7fffffffu;
-  return {max(max(u[0], u[1]), max(u[2], u[3])), max(max(u[4], u[5]), max(u[6], u[7]))};
+  for (int i = 0; i < E; ++i) {
+    t.a = max(t.a, __float_as_uint(r.w[i]) & 0x7fffffffu);
+    t.b = max(t.b, __float_as_uint(r.w[E + i]) & 0x7fffffffu);
+  }
+  return t;
 }
 
-// Writes the lane's eight elements in 8 bits. Side by side, four lanes hold a
-// block; with halves in chunks eight lanes' first chunks do, and their second
+// Writes the lane's elements in 8 bits. Side by side, 32 / 2E lanes hold a
+// block; with halves in chunks 32 / E lanes' first chunks do, and their second
 // chunks, where rot / 2 is a multiple of 32; for other rot the blocks' maxima
 // meet in shared memory.
-template <typename T, int PAIR, int ACC>
-__device__ __forceinline__ void write_codes(const QkArgs &A, const Part &P, int64_t row, const Lane &L,
-                                            bool on, uint32_t *tops, const Raw<T> &raw, const Row &x) {
+template <typename T, int E, int PAIR, int ACC>
+__device__ __forceinline__ void write_codes(const QkArgs &A, const Rows<uint8_t> &codes, uint8_t *scales,
+                                            int h, const Lane &L, bool on, uint32_t *tops,
+                                            const Raw<T, E> &raw, const Row<E> &x) {
   constexpr uint32_t kInf = 0x7f800000u;
-  Top t = chunk_tops(raw);
-  Row z = x;
+  Top t = chunk_tops<E>(raw);
+  if (ACC >= E) {
+    t.a = L.na > 0 ? t.a : 0;
+    t.b = L.nb > 0 ? t.b : 0;
+  }
+  Row<E> z = x;
   if (__any_sync(0xffffffffu, max(t.a, t.b) >= kInf)) {
     // what is not finite counts for nothing, and becomes NaN
     uint32_t u[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < E; ++i) {
       float2 f = unpair(x.v[i]);
+      uint32_t &top = u[i / (E / 2)];
       const uint32_t fx = __float_as_uint(f.x) & 0x7fffffffu, fy = __float_as_uint(f.y) & 0x7fffffffu;
-      if (fx < kInf) u[i / 2] = max(u[i / 2], fx);
+      if (fx < kInf) top = max(top, fx);
       else f.x = __int_as_float(0x7fffffff);
-      if (fy < kInf) u[i / 2] = max(u[i / 2], fy);
+      if (fy < kInf) top = max(top, fy);
       else f.y = __int_as_float(0x7fffffff);
       z.v[i] = pair(f.x, f.y);
     }
-    t = {u[0], u[1]};
+    t.a = ACC < E || L.na > 0 ? u[0] : 0;
+    t.b = ACC < E || L.nb > 0 ? u[1] : 0;
   }
   const bool split = PAIR == kPairSplit && L.a < A.rot;
   if (PAIR == kPairSplit && A.rot % 64) {
@@ -490,33 +550,41 @@ __device__ __forceinline__ void write_codes(const QkArgs &A, const Part &P, int6
     if (!split) t.a = t.b = max(t.a, t.b);
     if (PAIR == kPairSplit && sizeof(T) == 2) {          // both chunks' 16 bits in one word
       uint32_t w = __byte_perm(t.a, t.b, 0x7632);
-      w = __vmaxu2(w, __shfl_xor_sync(0xffffffffu, w, 1));
-      w = __vmaxu2(w, __shfl_xor_sync(0xffffffffu, w, 2));
-      const uint32_t o = __shfl_xor_sync(0xffffffffu, w, 4);
-      if (split) w = __vmaxu2(w, o);
+#pragma unroll
+      for (int off = 1; off < 32 / E; off <<= 1) {
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, w, off);
+        if (2 * off < 32 / E || split) w = max16x2(w, o);
+      }
       t = {w << 16, w & 0xffff0000u};
     } else {
 #pragma unroll
-      for (int off = 1; off < 8; off <<= 1) {
+      for (int off = 1; off < 32 / E; off <<= 1) {
+        const bool takes = 2 * off < 32 / E || split;
+        if (PAIR != kPairSplit && 2 * off >= 32 / E) break;
         const uint32_t oa = __shfl_xor_sync(0xffffffffu, t.a, off);
-        if (off < 4 || split) t.a = max(t.a, oa);
+        if (takes) t.a = max(t.a, oa);
         if (PAIR == kPairSplit) {
           const uint32_t ob = __shfl_xor_sync(0xffffffffu, t.b, off);
-          if (off < 4 || split) t.b = max(t.b, ob);
+          if (takes) t.b = max(t.b, ob);
         }
       }
     }
   }
   const int ea = block_exponent(t.a), eb = PAIR == kPairSplit ? block_exponent(t.b) : ea;
-  const uint32_t ca = encode4(z.v[0], z.v[1], ea), cb = encode4(z.v[2], z.v[3], eb);
-  if (!on) return;
-  uint8_t *p = P.codes + row * A.d, *e = P.scales + row * ((A.d + 31) / 32);
-  if (ACC == 8 && PAIR != kPairSplit) {
-    if (L.na > 0) *reinterpret_cast<uint2 *>(p + L.a) = make_uint2(ca, cb);
-  } else {
-    store_codes<ACC>(p + L.a, L.na, ca);
-    store_codes<ACC>(p + L.b, L.nb, cb);
+  const float ia = __uint_as_float(uint32_t(254 - ea) << 23);     // 2^-(ea - 127)
+  const float ib = __uint_as_float(uint32_t(254 - eb) << 23);
+  uint32_t c[E / 2];
+#pragma unroll
+  for (int i = 0; i < E; i += 2) {
+    const Pair inv = i < E / 2 ? pair(ia, ia) : pair(ib, ib);
+    const float2 f = unpair(mul2(z.v[i], inv)), g = unpair(mul2(z.v[i + 1], inv));
+    c[i / 2] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3) |
+               uint32_t(__nv_cvt_float2_to_fp8x2(g, __NV_SATFINITE, __NV_E4M3)) << 16;
   }
+  if (!on) return;
+  store_codes<E, ACC>(codes.first(h), L.na, c);
+  store_codes<E, ACC>(codes.second(h), L.nb, c + E / 4);
+  uint8_t *e = scales + int64_t(h) * ((A.d + 31) / 32);
   if ((L.a & 31) == 0 && L.na > 0) e[L.a / 32] = uint8_t(ea);
   if (PAIR == kPairSplit && (L.b & 31) == 0 && L.nb > 0) e[L.b / 32] = uint8_t(eb);
 }
@@ -533,56 +601,60 @@ __device__ __forceinline__ Item item_at(const QkArgs &A, int64_t item) {
 }
 
 // PACK: also write codes.
+constexpr int kFwdE = 8, kBwdE = 4;
 template <typename T, bool PACKED, bool PACK, int PAIR, int ACC>
-__global__ void __launch_bounds__(kQkThreads, 3) gdn_qk_fwd_kernel(const __grid_constant__ QkArgs A) {
-  constexpr int U = 4;
+__global__ void __launch_bounds__(kQkThreads, kFwdBlocksPerSm) gdn_qk_fwd_kernel(const __grid_constant__ QkArgs A) {
+  constexpr int E = kFwdE, U = 2;
   __shared__ __align__(16) float w_all[2][kMaxD];
   __shared__ __align__(16) float cs_all[PAIR == kPairNone ? 1 : kQkWarps][kMaxD];
-  __shared__ __align__(16) float rows_all[PAIR == kPairShared ? kQkWarps : 1][kMaxD];
-  __shared__ uint32_t tops_all[PACK && PAIR == kPairSplit ? kQkWarps * 32 : 1];
+  __shared__ __align__(16) float rows_all[PAIR == kPairShared ? kQkWarps : 1][2 * kMaxD];
+  __shared__ uint32_t tops_all[PACK && PAIR == kPairSplit ? kQkWarps * 64 : 1];
   const int G = 1 << A.lg, R = 32 >> A.lg;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> A.lg, l = lane & (G - 1);
   float *cs = cs_all[PAIR == kPairNone ? 0 : warp];
-  float *row_buf = rows_all[PAIR == kPairShared ? warp : 0] + (lane & -G) * 8;
-  uint32_t *tops = tops_all + (PACK && PAIR == kPairSplit ? warp * 32 + sub * 8 : 0);
-  const Lane L = lane_place<PAIR>(A, l);
+  float *row_buf = rows_all[PAIR == kPairShared ? warp : 0] + (lane & -G) * 2 * E;
+  uint32_t *tops = tops_all + (PACK && PAIR == kPairSplit ? warp * 64 + sub * 8 : 0);
+  const Lane L = lane_place<E, PAIR>(A, l);
   stage_weights<T>(A, true, true, w_all);
   const int64_t nwarps = int64_t(gridDim.x) * kQkWarps, items = int64_t(A.T) * A.splits;
   for (int64_t item = int64_t(blockIdx.x) * kQkWarps + warp; item < items; item += nwarps) {
     const Item I = item_at(A, item);
-    if (PAIR != kPairNone) make_angles(A, I.t, lane, cs);
+    if (PAIR != kPairNone) make_angles(A, I.t, lane, E << A.lg, cs);
     for (int part = 0; part < 2; ++part) {
       const Part &P = A.p[part];
       const int first = part ? A.p[0].H : 0;
       const int h0 = max(I.r0 - first, 0), h1 = min(I.r1 - first, P.H);
       if (h0 >= h1) continue;
-      Row C, S;
-      factors<PAIR>(A, L, l, cs, w_all[part], 1.f, C, S);
-      using Src = Source<T, PACKED, PAIR, ACC>;
-      Src src(A, P, I.t, h0 + sub, R);
-      T *out = static_cast<T *>(P.out) + I.t * P.out_ts + (h0 + sub) * P.out_hs;
-      const int64_t out_step = R * P.out_hs;
+      Row<E> C, S;
+      factors<E, PAIR>(A, L, l, cs, w_all[part], 1.f, C, S);
+      using Src = Source<T, PACKED, E, PAIR, ACC>;
+      const Src src(A, P, I.t, L);
+      const Rows<T> out(static_cast<T *>(P.out), I.t * P.out_ts, P.out_hs, L, false);
+      const int64_t row0 = int64_t(I.t) * P.H;
+      const Rows<uint8_t> codes(P.codes, row0 * A.d, A.d, L, false);
+      uint8_t *scales = PACK ? P.scales + row0 * ((A.d + 31) / 32) : nullptr;
       for (int h = h0 + sub; h - sub < h1; h += R * U) {
         typename Src::Data raw[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) src.load(L, h + u * R < h1, raw[u]);
+        for (int u = 0; u < U; ++u) src.load(min(h + u * R, h1 - 1), L, raw[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if (h - sub + u * R >= h1) break;
           const bool on = h + u * R < h1;
-          Row x;
-          unpack8(raw[u], x);
+          Row<E> x;
+          unpack(raw[u], x);
           if constexpr (PACK)
-            if (P.codes)
-              write_codes<T, PAIR, ACC>(A, P, int64_t(I.t) * P.H + h + u * R, L, on, tops, raw[u], x);
+            if (P.codes) write_codes<T, E, PAIR, ACC>(A, codes, scales, h + u * R, L, on, tops, raw[u], x);
           if (A.norm != GDN_NORM_NONE) {
-            const float r = rnorm(A, group_sum(dot8(x, x), A.lg));
+            const float r = rnorm(A, group_sum(dot<E, (ACC >= E)>(L, x, x), A.lg));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x.v[i] = mul2(x.v[i], pair(r, r));
+            for (int i = 0; i < E; ++i) x.v[i] = mul2(x.v[i], pair(r, r));
           }
-          turn<PAIR>(A, L, row_buf, C, S, x);
-          if (on && (!PACK || P.out)) store8<PAIR, ACC>(out, L, x);
-          out += out_step;
+          turn<E, PAIR>(A, L, row_buf, C, S, x);
+          if (on && (!PACK || P.out)) {
+            store_chunk<E, ACC>(out.first(h + u * R), L.na, x.v);
+            store_chunk<E, ACC>(out.second(h + u * R), L.nb, x.v + E / 2);
+          }
         }
       }
     }
@@ -591,78 +663,82 @@ __global__ void __launch_bounds__(kQkThreads, 3) gdn_qk_fwd_kernel(const __grid_
 
 // WEIGHTS: weights and their gradients.
 template <typename T, typename DT, bool PACKED, bool WEIGHTS, int PAIR, int ACC>
-__global__ void __launch_bounds__(kQkThreads, 2) gdn_qk_bwd_kernel(const __grid_constant__ QkArgs A) {
-  constexpr int U = 2;
+__global__ void __launch_bounds__(kQkThreads, kBwdBlocksPerSm) gdn_qk_bwd_kernel(const __grid_constant__ QkArgs A) {
+  constexpr int E = kBwdE, U = 2;
+  constexpr bool kWhole = ACC >= E;
   __shared__ __align__(16) float w_all[2][kMaxD], one[2][kMaxD];
   __shared__ __align__(16) float cs_all[PAIR == kPairNone ? 1 : kQkWarps][kMaxD];
   __shared__ __align__(16) float rows_all[PAIR == kPairShared || WEIGHTS ? kQkWarps : 1][kMaxD];
   const int G = 1 << A.lg, R = 32 >> A.lg;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> A.lg, l = lane & (G - 1);
   float *cs = cs_all[PAIR == kPairNone ? 0 : warp];
-  float *row_buf = rows_all[PAIR == kPairShared || WEIGHTS ? warp : 0] + (lane & -G) * 8;
-  const Lane L = lane_place<PAIR>(A, l);
+  float *row_buf = rows_all[PAIR == kPairShared || WEIGHTS ? warp : 0] + (lane & -G) * 2 * E;
+  const Lane L = lane_place<E, PAIR>(A, l);
   if (WEIGHTS) stage_weights<T>(A, false, true, w_all);
   stage_weights<T>(A, true, false, one);
   const int64_t nwarps = int64_t(gridDim.x) * kQkWarps, items = int64_t(A.T) * A.splits;
-  Row dw[2];
+  Row<E> dw[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dw[i / 4].v[i % 4] = pair(0.f, 0.f);
+  for (int i = 0; i < 2 * E; ++i) dw[i / E].v[i % E] = pair(0.f, 0.f);
   for (int64_t item = int64_t(blockIdx.x) * kQkWarps + warp; item < items; item += nwarps) {
     const Item I = item_at(A, item);
-    if (PAIR != kPairNone) make_angles(A, I.t, lane, cs);
+    if (PAIR != kPairNone) make_angles(A, I.t, lane, E << A.lg, cs);
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
       const Part &P = A.p[part];
       const int first = part ? A.p[0].H : 0;
       const int h0 = max(I.r0 - first, 0), h1 = min(I.r1 - first, P.H);
       if (h0 >= h1) continue;
-      Row C, S, W;
-      factors<PAIR>(A, L, l, cs, one[part], -1.f, C, S);
+      Row<E> C, S, W;
+      factors<E, PAIR>(A, L, l, cs, one[part], -1.f, C, S);
       if (WEIGHTS) {
-        const float4 wa = lds4(w_all[part] + L.a), wb = lds4(w_all[part] + L.b);
-        W.v[0] = pair(wa.x, wa.y); W.v[1] = pair(wa.z, wa.w);
-        W.v[2] = pair(wb.x, wb.y); W.v[3] = pair(wb.z, wb.w);
+        float w[2 * E];
+        lds<E>(w_all[part] + L.a, w);
+        lds<E>(w_all[part] + L.b, w + E);
+#pragma unroll
+        for (int i = 0; i < E; ++i) W.v[i] = pair(w[2 * i], w[2 * i + 1]);
       }
-      using Src = Source<T, PACKED, PAIR, ACC>;
-      Src src(A, P, I.t, h0 + sub, R);
-      const DT *dy = static_cast<const DT *>(P.dy) + I.t * P.dy_ts + (h0 + sub) * P.dy_hs;
-      T *out = static_cast<T *>(P.out) + I.t * P.out_ts + (h0 + sub) * P.out_hs;
-      const int64_t dy_step = R * P.dy_hs, out_step = R * P.out_hs;
+      using Src = Source<T, PACKED, E, PAIR, ACC>;
+      const Src src(A, P, I.t, L);
+      const Rows<const DT> dy(static_cast<const DT *>(P.dy), I.t * P.dy_ts, P.dy_hs, L, true);
+      const Rows<T> out(static_cast<T *>(P.out), I.t * P.out_ts, P.out_hs, L, false);
       for (int h = h0 + sub; h - sub < h1; h += R * U) {
         typename Src::Data raw[U];
-        Raw<DT> grad[U];
+        Raw<DT, E> grad[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          src.load(L, h + u * R < h1, raw[u]);
-          load8<PAIR, ACC>(dy, L, h + u * R < h1, grad[u]);
-          dy += dy_step;
+          const int hu = min(h + u * R, h1 - 1);
+          src.load(hu, L, raw[u]);
+          load_row<E, ACC>(dy, hu, L, grad[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if (h - sub + u * R >= h1) break;
-          Row x, z;
-          unpack8(raw[u], x);
-          unpack8(grad[u], z);
-          turn<PAIR>(A, L, row_buf, C, S, z);
+          const bool on = h + u * R < h1;
+          Row<E> x, z;
+          unpack(raw[u], x);
+          unpack(grad[u], z);
+          turn<E, PAIR>(A, L, row_buf, C, S, z);
           float r = 1.f, m = 0.f;
-          Row dh = z;
+          Row<E> dh = z;
           if (WEIGHTS) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dh.v[i] = mul2(z.v[i], W.v[i]);
+            for (int i = 0; i < E; ++i) dh.v[i] = mul2(z.v[i], W.v[i]);
           }
           if (A.norm != GDN_NORM_NONE) {
-            r = rnorm(A, group_sum(dot8(x, x), A.lg));
-            m = group_sum(dot8(x, dh), A.lg) * r * A.inv_n;
+            r = rnorm(A, group_sum(dot<E, kWhole>(L, x, x), A.lg));
+            m = group_sum(dot<E, kWhole>(L, x, dh), A.lg) * r * A.inv_n;
           }
           const Pair rr = pair(r, r), mm = pair(-m, -m);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const Pair hx = mul2(x.v[i], rr);
-            if (WEIGHTS) dw[part].v[i] = fma2(z.v[i], hx, dw[part].v[i]);
-            x.v[i] = A.norm == GDN_NORM_NONE ? dh.v[i] : mul2(fma2(hx, mm, dh.v[i]), rr);
+          for (int i = 0; i < E; ++i) {
+            if (WEIGHTS && on) dw[part].v[i] = fma2(z.v[i], mul2(x.v[i], rr), dw[part].v[i]);
+            x.v[i] = A.norm == GDN_NORM_NONE ? dh.v[i] : mul2(fma2(mul2(x.v[i], rr), mm, dh.v[i]), rr);
           }
-          if (h + u * R < h1) store8<PAIR, ACC>(out, L, x);
-          out += out_step;
+          if (on) {
+            store_chunk<E, ACC>(out.first(h + u * R), L.na, x.v);
+            store_chunk<E, ACC>(out.second(h + u * R), L.nb, x.v + E / 2);
+          }
         }
       }
     }
@@ -672,15 +748,15 @@ __global__ void __launch_bounds__(kQkThreads, 2) gdn_qk_bwd_kernel(const __grid_
     for (int part = 0; part < 2; ++part) {
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 2 * E; ++i) {
         const float2 f = unpair(dw[part].v[i / 2]);
-        const int e = element(L, i);
-        if (e < G * 8) row_buf[e] = i & 1 ? f.y : f.x;
+        const int e = i < E ? L.a + i : L.b + i - E;
+        if (e < A.d) row_buf[e] = i & 1 ? f.y : f.x;
       }
       __syncthreads();
       for (int e = threadIdx.x; e < A.d; e += kQkThreads) {
         float s = 0.f;
-        for (int i = 0; i < kQkWarps * R; ++i) s += rows_all[i / R][(i % R) * G * 8 + e];
+        for (int i = 0; i < kQkWarps * R; ++i) s += rows_all[i / R][(i % R) * G * 2 * E + e];
         A.dw_part[(int64_t(part) * gridDim.x + blockIdx.x) * A.d + e] = s;
       }
     }
@@ -706,18 +782,18 @@ __global__ void __launch_bounds__(1024) gdn_qk_dw_kernel(const float *part, int 
 
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// Elements per access: the most that every pointer and stride allows.
-int access_width(const QkArgs &A, size_t xe, size_t dye, bool packed) {
+// Elements per access: the most that every pointer and stride (in bytes) allows.
+int access_width(const QkArgs &A, int xe, int dye, bool packed) {
   for (int acc = 8; acc > 1; acc -= 4) {
     if (A.d % acc) continue;
     bool ok = true;
     for (const Part &P : A.p) {
       if (!P.H) continue;
-      const size_t xb = xe == 4 ? 16 : acc * xe, db = dye == 4 ? 16 : acc * dye;
+      const int xb = xe == 4 ? 16 : acc * xe, db = dye == 4 ? 16 : acc * dye;
       if (packed) ok &= aligned(P.x, acc);
-      else ok &= aligned(P.x, xb) && P.x_ts % acc == 0 && P.x_hs % acc == 0;
-      if (P.dy) ok &= aligned(P.dy, db) && P.dy_ts % acc == 0 && P.dy_hs % acc == 0;
-      if (P.out) ok &= aligned(P.out, xb) && P.out_ts % acc == 0 && P.out_hs % acc == 0;
+      else ok &= aligned(P.x, xb) && P.x_ts % xb == 0 && P.x_hs % xb == 0;
+      if (P.dy) ok &= aligned(P.dy, db) && P.dy_ts % db == 0 && P.dy_hs % db == 0;
+      if (P.out) ok &= aligned(P.out, xb) && P.out_ts % xb == 0 && P.out_hs % xb == 0;
       if (P.codes) ok &= aligned(P.codes, acc);
     }
     if (ok) return acc;
@@ -726,18 +802,17 @@ int access_width(const QkArgs &A, size_t xe, size_t dye, bool packed) {
 }
 
 // The way the pairs are handled: halves go in chunks where they fall into them.
-int pair_mode(const gdn_qk_params *p, int acc) {
+int pair_mode(const gdn_qk_params *p, int acc, int e) {
   if (!p->rot) return kPairNone;
   if (p->interleaved) return kPairInterleaved;
-  return acc >= 4 && p->rot % 8 == 0 ? kPairSplit : kPairShared;
+  return acc >= 4 && p->rot % (2 * e) == 0 ? kPairSplit : kPairShared;
 }
-
-constexpr int kFwdBlocksPerSm = 3, kBwdBlocksPerSm = 2;
 
 // Rows an item and items a token: whole tokens, whose cosines then serve every
 // head, where there are enough of them for all warps; else fewer rows, down to
 // one step of a warp.
-unsigned plan(QkArgs &A, int per_sm) {
+unsigned plan(QkArgs &A, int e, int per_sm) {
+  for (A.lg = 2; (2 * e) << A.lg < A.d; ++A.lg) {}
   const int rows = A.p[0].H + A.p[1].H, step = 32 >> A.lg, sms = device_sms();
   const int64_t warps = int64_t(sms > 0 ? sms : 1) * per_sm * kQkWarps;
   int64_t want = (int64_t(A.T) * rows + warps - 1) / warps;          // rows a warp
@@ -749,28 +824,33 @@ unsigned plan(QkArgs &A, int per_sm) {
   return unsigned(blocks < 1 ? 1 : blocks < most ? blocks : most);
 }
 
-// Turns the run-time choices into template arguments: a variant for each way
-// the pairs lie, at the widest access (16 bytes of T where eight elements lie
-// side by side) and narrower ones.
+// Turns the run-time choices into template arguments. Accesses of eight
+// elements: a chunk of eight (E = 8), or two chunks of four side by side.
 template <int V> struct Const { static constexpr int value = V; };
-template <typename T, typename F>
+template <int E, typename F>
 void with_variant(int pair, int acc, F f) {
   auto pick = [&](auto a) {
     if (pair == kPairNone) f(Const<kPairNone>{}, a);
     else if (pair == kPairInterleaved) f(Const<kPairInterleaved>{}, a);
     else f(Const<kPairShared>{}, a);
   };
-  if (pair == kPairSplit) f(Const<kPairSplit>{}, Const<4>{});
-  else if (acc == 8 && sizeof(T) == 2) pick(Const<8>{});
-  else if (acc >= 4) pick(Const<4>{});
-  else pick(Const<1>{});
+  if (pair == kPairSplit) {
+    if (E == 8 && acc == 8) f(Const<kPairSplit>{}, Const<E>{});
+    else f(Const<kPairSplit>{}, Const<4>{});
+  } else if (acc == 8) {
+    pick(Const<8>{});
+  } else if (acc >= 4) {
+    pick(Const<4>{});
+  } else {
+    pick(Const<1>{});
+  }
 }
 
 template <bool PACKED, bool PACK>
 cudaError_t fwd_launch(const QkArgs &A, int dtype, int pair, int acc, unsigned grid, cudaStream_t s) {
   auto go = [&](auto type) {
     using T = decltype(type);
-    with_variant<T>(pair, acc, [&](auto p, auto a) {
+    with_variant<kFwdE>(pair, acc, [&](auto p, auto a) {
       gdn_qk_fwd_kernel<T, PACKED, PACK, decltype(p)::value, decltype(a)::value>
           <<<grid, kQkThreads, 0, s>>>(A);
     });
@@ -785,7 +865,7 @@ cudaError_t bwd_launch(const QkArgs &A, int dtype, int grad_dtype, int pair, int
   auto go = [&](auto type, auto grad) {
     using T = decltype(type);
     using DT = decltype(grad);
-    with_variant<T>(pair, acc, [&](auto p, auto a) {
+    with_variant<kBwdE>(pair, acc, [&](auto p, auto a) {
       gdn_qk_bwd_kernel<T, DT, PACKED, WEIGHTS, decltype(p)::value, decltype(a)::value>
           <<<grid, kQkThreads, 0, s>>>(A);
     });
@@ -811,7 +891,7 @@ int check_params(const gdn_qk_params *p) {
 }
 
 bool rows_ok(const gdn_rows *r, int H, int d, size_t e) {
-  return r && r->data && aligned(r->data, e) && r->head_stride >= d &&
+  return r && r->data && aligned(r->data, e) && r->head_stride >= d && r->head_stride < (1 << 28) &&
          r->token_stride >= (H > 0 ? int64_t(H - 1) * r->head_stride + d : 0);
 }
 
@@ -823,7 +903,6 @@ int fill(QkArgs &A, const gdn_qk_params *p, const gdn_rows *const x[2],
   A.inv_freq = p->inv_freq;
   A.T = p->T; A.d = p->d; A.rot = p->rot; A.norm = p->norm;
   A.eps = p->eps; A.w0 = p->weight_offset; A.rope_scale = p->rope_scale;
-  A.lg = p->d <= 64 ? 3 : p->d <= 128 ? 4 : 5;
   A.inv_n = p->norm == GDN_NORM_RMS ? 1.f / float(p->d) : 1.f;
   for (int i = 0; i < 2; ++i) {
     Part &P = A.p[i];
@@ -837,11 +916,11 @@ int fill(QkArgs &A, const gdn_qk_params *p, const gdn_rows *const x[2],
       P.x_scales = x8[i]->scales;
     } else {
       if (!rows_ok(x[i], P.H, p->d, e)) return GDN_ERR_INVALID_ARG;
-      P.x = x[i]->data; P.x_ts = x[i]->token_stride; P.x_hs = x[i]->head_stride;
+      P.x = x[i]->data; P.x_ts = x[i]->token_stride * e; P.x_hs = int(x[i]->head_stride * e);
     }
     if (dy) {
       if (!rows_ok(dy[i], P.H, p->d, dye)) return GDN_ERR_INVALID_ARG;
-      P.dy = dy[i]->data; P.dy_ts = dy[i]->token_stride; P.dy_hs = dy[i]->head_stride;
+      P.dy = dy[i]->data; P.dy_ts = dy[i]->token_stride * dye; P.dy_hs = int(dy[i]->head_stride * dye);
     }
     if (out8 && out8[i] && out8[i]->codes) {
       if (!out8[i]->scales) return GDN_ERR_INVALID_ARG;
@@ -850,7 +929,7 @@ int fill(QkArgs &A, const gdn_qk_params *p, const gdn_rows *const x[2],
     }
     if (out[i] && out[i]->data) {
       if (!rows_ok(out[i], P.H, p->d, e)) return GDN_ERR_INVALID_ARG;
-      P.out = out[i]->data; P.out_ts = out[i]->token_stride; P.out_hs = out[i]->head_stride;
+      P.out = out[i]->data; P.out_ts = out[i]->token_stride * e; P.out_hs = int(out[i]->head_stride * e);
     } else if (!P.codes) {
       return GDN_ERR_INVALID_ARG;
     }
@@ -868,10 +947,10 @@ int run_fwd(const gdn_qk_params *p, const gdn_rows *const x[2], const gdn_packed
   if (rc != GDN_OK) return rc;
   if (!A.p[0].H && !A.p[1].H) return GDN_OK;
   const bool pack = A.p[0].codes || A.p[1].codes;
-  const unsigned grid = plan(A, kFwdBlocksPerSm);
+  const unsigned grid = plan(A, kFwdE, kFwdBlocksPerSm);
   const int acc = access_width(A, p->dtype == GDN_BF16 ? 2 : 4, 2, PACKED);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int pair = pair_mode(p, acc);
+  const int pair = pair_mode(p, acc, kFwdE);
   cudaError_t e;
   if constexpr (PACKED) e = fwd_launch<true, false>(A, p->dtype, pair, acc, grid, s);
   else if (pack) e = fwd_launch<false, true>(A, p->dtype, pair, acc, grid, s);
@@ -895,11 +974,11 @@ int run_bwd(const gdn_qk_params *p, const gdn_rows *const dy[2], int grad_dtype,
   rc = fill(A, p, x, PACKED ? x8 : nullptr, dy, grad_dtype == GDN_BF16 ? 2 : 4, out, nullptr);
   if (rc != GDN_OK) return rc;
   A.dw_part = static_cast<float *>(ws);
-  const unsigned grid = plan(A, kBwdBlocksPerSm);
+  const unsigned grid = plan(A, kBwdE, kBwdBlocksPerSm);
   const int acc = access_width(A, p->dtype == GDN_BF16 ? 2 : 4, grad_dtype == GDN_BF16 ? 2 : 4, PACKED);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!A.p[0].H && !A.p[1].H && !dw_q && !dw_k) return GDN_OK;
-  const int pair = pair_mode(p, acc);
+  const int pair = pair_mode(p, acc, kBwdE);
   const cudaError_t e =
       dw_q || dw_k ? bwd_launch<PACKED, true>(A, p->dtype, grad_dtype, pair, acc, grid, s)
                    : bwd_launch<PACKED, false>(A, p->dtype, grad_dtype, pair, acc, grid, s);
