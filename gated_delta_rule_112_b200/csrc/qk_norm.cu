@@ -183,17 +183,24 @@ __device__ __forceinline__ void unpack(const Raw<float, E> &r, Row<E> &x) {
 __device__ __forceinline__ float pow2_biased(uint32_t b) {
   return __uint_as_float(b ? b << 23 : 0x00400000u);
 }
+// Codes without their scales, which go into the row's sums and factor.
 template <int E>
 __device__ __forceinline__ void unpack(const Codes<E> &r, Row<E> &x) {
-  const float sa = pow2_biased(r.ea), sb = pow2_biased(r.eb);
 #pragma unroll
   for (int i = 0; i < E; ++i) {
-    const float s = i < E / 2 ? sa : sb;
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
         static_cast<__nv_fp8x2_storage_t>((r.w[i / 2] >> (16 * (i & 1))) & 0xffff), __NV_E4M3);
     const float2 f = __half22float2(__half2(h));
-    x.v[i] = mul2(pair(f.x, f.y), pair(s, s));
+    x.v[i] = pair(f.x, f.y);
   }
+}
+// What the unpacked chunks are to be multiplied by.
+struct Scales { float a, b; };
+template <typename D>
+__device__ __forceinline__ Scales scales_of(const D &) { return {1.f, 1.f}; }
+template <int E>
+__device__ __forceinline__ Scales scales_of(const Codes<E> &r) {
+  return {pow2_biased(r.ea), pow2_biased(r.eb)};
 }
 
 template <int E, int ACC>
@@ -278,8 +285,10 @@ __device__ __forceinline__ void load_row(const Rows<const T> &P, int h, const La
   }
 }
 
-// Sum over the 2^lg lanes of a row.
+// Sum over the 2^lg lanes of a row; LG: lg where the compiler knows it, else 0.
+template <int LG>
 __device__ __forceinline__ float group_sum(float x, int lg) {
+  if (LG) lg = LG;
   if (lg > 4) x += __shfl_xor_sync(0xffffffffu, x, 16);
   if (lg > 3) x += __shfl_xor_sync(0xffffffffu, x, 8);
   if (lg > 2) x += __shfl_xor_sync(0xffffffffu, x, 4);
@@ -287,9 +296,9 @@ __device__ __forceinline__ float group_sum(float x, int lg) {
   x += __shfl_xor_sync(0xffffffffu, x, 1);
   return x;
 }
-// x . y over the lane's elements; chunks that do not exist count for nothing.
+// x . y over each of the lane's chunks; chunks that do not exist count for nothing.
 template <int E, bool WHOLE>
-__device__ __forceinline__ float dot(const Lane &L, const Row<E> &x, const Row<E> &y) {
+__device__ __forceinline__ float2 dots(const Lane &L, const Row<E> &x, const Row<E> &y) {
   Pair s = mul2(x.v[0], y.v[0]), t = mul2(x.v[E / 2], y.v[E / 2]);
 #pragma unroll
   for (int i = 1; i < E / 2; ++i) {
@@ -297,12 +306,12 @@ __device__ __forceinline__ float dot(const Lane &L, const Row<E> &x, const Row<E
     t = fma2(x.v[E / 2 + i], y.v[E / 2 + i], t);
   }
   const float2 f = unpair(s), g = unpair(t);
-  float a = f.x + f.y, b = g.x + g.y;
+  float2 d = make_float2(f.x + f.y, g.x + g.y);
   if (WHOLE) {
-    a = L.na > 0 ? a : 0.f;
-    b = L.nb > 0 ? b : 0.f;
+    if (L.na == 0) d.x = 0.f;
+    if (L.nb == 0) d.y = 0.f;
   }
-  return a + b;
+  return d;
 }
 
 // The lane's part of x C + x' S, x' the partner of every element. What does
@@ -473,12 +482,12 @@ __device__ __forceinline__ int block_exponent(uint32_t bits) {
   return max(int((bits + 0x1fffffu) >> 23) - 8, 0);
 }
 // Largest magnitude of each chunk, as bits of an fp32: of non-negative floats
-// the bits compare alike, with infinities and NaN above the rest. bf16 compares
-// two at a time in 16 bits.
+// the bits compare alike, with infinities and NaN above the rest. bf16 is
+// compared two at a time (a NaN wins).
 struct Top { uint32_t a, b; };
-__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 template <int E>
@@ -487,10 +496,10 @@ __device__ __forceinline__ Top chunk_tops(const Raw<__nv_bfloat16, E> &r) {
   uint32_t a = r.w[0] & m, b = r.w[E / 2] & m;
 #pragma unroll
   for (int i = 1; i < E / 2; ++i) {
-    a = max16x2(a, r.w[i] & m);
-    b = max16x2(b, r.w[E / 2 + i] & m);
+    a = max2(a, r.w[i] & m);
+    b = max2(b, r.w[E / 2 + i] & m);
   }
-  const uint32_t t = max16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+  const uint32_t t = max2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
   return {t << 16, t & 0xffff0000u};
 }
 template <int E>
@@ -553,7 +562,7 @@ __device__ __forceinline__ void write_codes(const QkArgs &A, const Rows<uint8_t>
 #pragma unroll
       for (int off = 1; off < 32 / E; off <<= 1) {
         const uint32_t o = __shfl_xor_sync(0xffffffffu, w, off);
-        if (2 * off < 32 / E || split) w = max16x2(w, o);
+        if (2 * off < 32 / E || split) w = max2(w, o);
       }
       t = {w << 16, w & 0xffff0000u};
     } else {
@@ -602,15 +611,15 @@ __device__ __forceinline__ Item item_at(const QkArgs &A, int64_t item) {
 
 // PACK: also write codes.
 constexpr int kFwdE = 8, kBwdE = 4;
-template <typename T, bool PACKED, bool PACK, int PAIR, int ACC>
+template <typename T, bool PACKED, bool PACK, int PAIR, int ACC, int LG>
 __global__ void __launch_bounds__(kQkThreads, kFwdBlocksPerSm) gdn_qk_fwd_kernel(const __grid_constant__ QkArgs A) {
-  constexpr int E = kFwdE, U = 2;
+  constexpr int E = kFwdE, U = 4;
   __shared__ __align__(16) float w_all[2][kMaxD];
   __shared__ __align__(16) float cs_all[PAIR == kPairNone ? 1 : kQkWarps][kMaxD];
   __shared__ __align__(16) float rows_all[PAIR == kPairShared ? kQkWarps : 1][2 * kMaxD];
   __shared__ uint32_t tops_all[PACK && PAIR == kPairSplit ? kQkWarps * 64 : 1];
-  const int G = 1 << A.lg, R = 32 >> A.lg;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> A.lg, l = lane & (G - 1);
+  const int lg = LG ? LG : A.lg, G = 1 << lg, R = 32 >> lg;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> lg, l = lane & (G - 1);
   float *cs = cs_all[PAIR == kPairNone ? 0 : warp];
   float *row_buf = rows_all[PAIR == kPairShared ? warp : 0] + (lane & -G) * 2 * E;
   uint32_t *tops = tops_all + (PACK && PAIR == kPairSplit ? warp * 64 + sub * 8 : 0);
@@ -619,7 +628,7 @@ __global__ void __launch_bounds__(kQkThreads, kFwdBlocksPerSm) gdn_qk_fwd_kernel
   const int64_t nwarps = int64_t(gridDim.x) * kQkWarps, items = int64_t(A.T) * A.splits;
   for (int64_t item = int64_t(blockIdx.x) * kQkWarps + warp; item < items; item += nwarps) {
     const Item I = item_at(A, item);
-    if (PAIR != kPairNone) make_angles(A, I.t, lane, E << A.lg, cs);
+    if (PAIR != kPairNone) make_angles(A, I.t, lane, E << lg, cs);
     for (int part = 0; part < 2; ++part) {
       const Part &P = A.p[part];
       const int first = part ? A.p[0].H : 0;
@@ -643,12 +652,21 @@ __global__ void __launch_bounds__(kQkThreads, kFwdBlocksPerSm) gdn_qk_fwd_kernel
           const bool on = h + u * R < h1;
           Row<E> x;
           unpack(raw[u], x);
+          Scales sc = scales_of(raw[u]);
           if constexpr (PACK)
             if (P.codes) write_codes<T, E, PAIR, ACC>(A, codes, scales, h + u * R, L, on, tops, raw[u], x);
           if (A.norm != GDN_NORM_NONE) {
-            const float r = rnorm(A, group_sum(dot<E, (ACC >= E)>(L, x, x), A.lg));
+            const float2 d = dots<E, (ACC >= E)>(L, x, x);
+            // (d s) s and not d s^2, which could leave the range where the sum does not
+            const float ss = PACKED ? d.x * sc.a * sc.a + d.y * sc.b * sc.b : d.x + d.y;
+            const float r = rnorm(A, group_sum<LG>(ss, A.lg));
+            sc.a *= r;
+            sc.b *= r;
+          }
+          if (PACKED || A.norm != GDN_NORM_NONE) {
 #pragma unroll
-            for (int i = 0; i < E; ++i) x.v[i] = mul2(x.v[i], pair(r, r));
+            for (int i = 0; i < E; ++i)
+              x.v[i] = mul2(x.v[i], i < E / 2 || !PACKED ? pair(sc.a, sc.a) : pair(sc.b, sc.b));
           }
           turn<E, PAIR>(A, L, row_buf, C, S, x);
           if (on && (!PACK || P.out)) {
@@ -662,15 +680,15 @@ __global__ void __launch_bounds__(kQkThreads, kFwdBlocksPerSm) gdn_qk_fwd_kernel
 }
 
 // WEIGHTS: weights and their gradients.
-template <typename T, typename DT, bool PACKED, bool WEIGHTS, int PAIR, int ACC>
+template <typename T, typename DT, bool PACKED, bool WEIGHTS, int PAIR, int ACC, int LG>
 __global__ void __launch_bounds__(kQkThreads, kBwdBlocksPerSm) gdn_qk_bwd_kernel(const __grid_constant__ QkArgs A) {
   constexpr int E = kBwdE, U = 2;
   constexpr bool kWhole = ACC >= E;
   __shared__ __align__(16) float w_all[2][kMaxD], one[2][kMaxD];
   __shared__ __align__(16) float cs_all[PAIR == kPairNone ? 1 : kQkWarps][kMaxD];
   __shared__ __align__(16) float rows_all[PAIR == kPairShared || WEIGHTS ? kQkWarps : 1][kMaxD];
-  const int G = 1 << A.lg, R = 32 >> A.lg;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> A.lg, l = lane & (G - 1);
+  const int lg = LG ? LG : A.lg, G = 1 << lg, R = 32 >> lg;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> lg, l = lane & (G - 1);
   float *cs = cs_all[PAIR == kPairNone ? 0 : warp];
   float *row_buf = rows_all[PAIR == kPairShared || WEIGHTS ? warp : 0] + (lane & -G) * 2 * E;
   const Lane L = lane_place<E, PAIR>(A, l);
@@ -682,7 +700,7 @@ __global__ void __launch_bounds__(kQkThreads, kBwdBlocksPerSm) gdn_qk_bwd_kernel
   for (int i = 0; i < 2 * E; ++i) dw[i / E].v[i % E] = pair(0.f, 0.f);
   for (int64_t item = int64_t(blockIdx.x) * kQkWarps + warp; item < items; item += nwarps) {
     const Item I = item_at(A, item);
-    if (PAIR != kPairNone) make_angles(A, I.t, lane, E << A.lg, cs);
+    if (PAIR != kPairNone) make_angles(A, I.t, lane, E << lg, cs);
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
       const Part &P = A.p[part];
@@ -718,6 +736,7 @@ __global__ void __launch_bounds__(kQkThreads, kBwdBlocksPerSm) gdn_qk_bwd_kernel
           Row<E> x, z;
           unpack(raw[u], x);
           unpack(grad[u], z);
+          Scales sc = scales_of(raw[u]);
           turn<E, PAIR>(A, L, row_buf, C, S, z);
           float r = 1.f, m = 0.f;
           Row<E> dh = z;
@@ -726,14 +745,19 @@ __global__ void __launch_bounds__(kQkThreads, kBwdBlocksPerSm) gdn_qk_bwd_kernel
             for (int i = 0; i < E; ++i) dh.v[i] = mul2(z.v[i], W.v[i]);
           }
           if (A.norm != GDN_NORM_NONE) {
-            r = rnorm(A, group_sum(dot<E, kWhole>(L, x, x), A.lg));
-            m = group_sum(dot<E, kWhole>(L, x, dh), A.lg) * r * A.inv_n;
+            const float2 d = dots<E, kWhole>(L, x, x), e = dots<E, kWhole>(L, x, dh);
+            const float ss = PACKED ? d.x * sc.a * sc.a + d.y * sc.b * sc.b : d.x + d.y;
+            const float xd = PACKED ? e.x * sc.a + e.y * sc.b : e.x + e.y;
+            r = rnorm(A, group_sum<LG>(ss, A.lg));
+            m = group_sum<LG>(xd, A.lg) * r * A.inv_n;
           }
           const Pair rr = pair(r, r), mm = pair(-m, -m);
+          const Pair ra = pair(r * sc.a, r * sc.a), rb = PACKED ? pair(r * sc.b, r * sc.b) : ra;
 #pragma unroll
           for (int i = 0; i < E; ++i) {
-            if (WEIGHTS && on) dw[part].v[i] = fma2(z.v[i], mul2(x.v[i], rr), dw[part].v[i]);
-            x.v[i] = A.norm == GDN_NORM_NONE ? dh.v[i] : mul2(fma2(mul2(x.v[i], rr), mm, dh.v[i]), rr);
+            const Pair hx = mul2(x.v[i], i < E / 2 ? ra : rb);
+            if (WEIGHTS && on) dw[part].v[i] = fma2(z.v[i], hx, dw[part].v[i]);
+            x.v[i] = A.norm == GDN_NORM_NONE ? dh.v[i] : mul2(fma2(hx, mm, dh.v[i]), rr);
           }
           if (on) {
             store_chunk<E, ACC>(out.first(h + u * R), L.na, x.v);
@@ -828,30 +852,31 @@ unsigned plan(QkArgs &A, int e, int per_sm) {
 // elements: a chunk of eight (E = 8), or two chunks of four side by side.
 template <int V> struct Const { static constexpr int value = V; };
 template <int E, typename F>
-void with_variant(int pair, int acc, F f) {
-  auto pick = [&](auto a) {
-    if (pair == kPairNone) f(Const<kPairNone>{}, a);
-    else if (pair == kPairInterleaved) f(Const<kPairInterleaved>{}, a);
-    else f(Const<kPairShared>{}, a);
+void with_variant(int pair, int acc, int lg, F f) {
+  // The common width of a head, 65 to 128 elements, is known to the compiler
+  // where the accesses are wide.
+  constexpr int known = E == 8 ? 3 : 4;
+  auto pick = [&](auto a, auto g) {
+    constexpr int wide = decltype(a)::value, split = wide >= E ? E : 4;
+    if (pair == kPairNone) f(Const<kPairNone>{}, a, g);
+    else if (pair == kPairInterleaved) f(Const<kPairInterleaved>{}, a, g);
+    else if (pair == kPairSplit) f(Const<kPairSplit>{}, Const<split>{}, g);
+    else f(Const<kPairShared>{}, a, Const<0>{});
   };
-  if (pair == kPairSplit) {
-    if (E == 8 && acc == 8) f(Const<kPairSplit>{}, Const<E>{});
-    else f(Const<kPairSplit>{}, Const<4>{});
-  } else if (acc == 8) {
-    pick(Const<8>{});
-  } else if (acc >= 4) {
-    pick(Const<4>{});
-  } else {
-    pick(Const<1>{});
-  }
+  if (acc == 8 && lg == known) pick(Const<8>{}, Const<known>{});
+  else if (acc == 8) pick(Const<8>{}, Const<0>{});
+  else if (acc >= 4) pick(Const<4>{}, Const<0>{});
+  else if (pair == kPairNone) f(Const<kPairNone>{}, Const<1>{}, Const<0>{});
+  else if (pair == kPairInterleaved) f(Const<kPairInterleaved>{}, Const<1>{}, Const<0>{});
+  else f(Const<kPairShared>{}, Const<1>{}, Const<0>{});
 }
 
 template <bool PACKED, bool PACK>
 cudaError_t fwd_launch(const QkArgs &A, int dtype, int pair, int acc, unsigned grid, cudaStream_t s) {
   auto go = [&](auto type) {
     using T = decltype(type);
-    with_variant<kFwdE>(pair, acc, [&](auto p, auto a) {
-      gdn_qk_fwd_kernel<T, PACKED, PACK, decltype(p)::value, decltype(a)::value>
+    with_variant<kFwdE>(pair, acc, A.lg, [&](auto p, auto a, auto g) {
+      gdn_qk_fwd_kernel<T, PACKED, PACK, decltype(p)::value, decltype(a)::value, decltype(g)::value>
           <<<grid, kQkThreads, 0, s>>>(A);
     });
   };
@@ -865,8 +890,8 @@ cudaError_t bwd_launch(const QkArgs &A, int dtype, int grad_dtype, int pair, int
   auto go = [&](auto type, auto grad) {
     using T = decltype(type);
     using DT = decltype(grad);
-    with_variant<kBwdE>(pair, acc, [&](auto p, auto a) {
-      gdn_qk_bwd_kernel<T, DT, PACKED, WEIGHTS, decltype(p)::value, decltype(a)::value>
+    with_variant<kBwdE>(pair, acc, A.lg, [&](auto p, auto a, auto g) {
+      gdn_qk_bwd_kernel<T, DT, PACKED, WEIGHTS, decltype(p)::value, decltype(a)::value, decltype(g)::value>
           <<<grid, kQkThreads, 0, s>>>(A);
     });
   };
