@@ -9,6 +9,7 @@ calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import NamedTuple
@@ -384,59 +385,85 @@ def recurrent_fwd(q, k, v, g, beta, pool, slots=None, cu_seqlens=None, keep=None
     [N]) starts it from zero. Tokens of no run keep what ``out`` held.
     A run the device finds wrong (see gdn.h) leaves its state alone and has NaN
     outputs; ``status`` (see ``status_block``) then tells get_status."""
-    dev = _one_device(q, k, v, g, beta, pool, slots, cu_seqlens, keep, reset, out, status)
-    T, Hk, dk = q.shape
-    Hv, dv = v.shape[1], v.shape[2]
     name = "gdn_recurrent_fwd"
-    _require(name, k.shape == q.shape and v.shape[0] == T, "q, k, v shapes")
-    _require(name, q.dtype == k.dtype == v.dtype, "q, k, v have one dtype")
+    dev = q.get_device()
+    if dev < 0 or stream is not None or dev != torch.cuda.current_device():
+        with _on(name, dev, stream):
+            return recurrent_fwd(q, k, v, g, beta, pool, slots, cu_seqlens, keep, reset, out, status)
+    T, Hk, dk = q.shape
+    _, Hv, dv = v.shape
+    P = pool.shape[0]
     channel = g.dim() == 3
-    _require(name, tuple(g.shape) == ((T, Hv, dk) if channel else (T, Hv)), "shape of g")
-    _require(name, tuple(beta.shape) == (T, Hv), "shape of beta")
-    _require(name, pool.dim() == 4 and tuple(pool.shape[1:]) == (Hv, dk, dv), "shape of pool")
-    _require(name, all(x.dtype == torch.float32 and x.is_contiguous() for x in (g, beta)),
-             "g, beta are contiguous fp32")
-    _require(name, pool.is_contiguous(), "pool is contiguous")
-    N = (cu_seqlens.numel() - 1 if cu_seqlens is not None else
-         slots.numel() if slots is not None else pool.shape[0])
-    for x, t, n in ((slots, torch.int32, N), (cu_seqlens, torch.int32, N + 1),
-                    (keep, torch.int32, N), (reset, torch.bool, N)):
-        _require(name, x is None or (x.dtype == t and x.numel() == n and x.is_contiguous()),
-                 f"an index array is not contiguous {t} of {n}")
-    _require(name, status is None or (status.numel() * status.element_size() >= 256), "status")
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
-        if out is None:
-            out = torch.empty(T, Hv, dv, dtype=q.dtype, device=dev)
-        _require(name, tuple(out.shape) == (T, Hv, dv) and out.dtype == q.dtype and
-                 out.is_contiguous(), "out")
-        rc = lib().gdn_recurrent_fwd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(pool), _ptr(slots),
-            _ptr(cu_seqlens), _ptr(keep), _ptr(reset), N, T, Hk, Hv, dk, dv, pool.shape[0],
-            _token_stride(name, q), _token_stride(name, k), _token_stride(name, v), int(channel),
-            _dtype_code(q.dtype), _dtype_code(pool.dtype), _ptr(out), _ptr(status),
-            _stream_ptr(stream))
-    _check(rc, name)
+    dt, st = q.dtype, pool.dtype
+    if cu_seqlens is not None:
+        N = cu_seqlens.numel() - 1
+    else:
+        N = slots.numel() if slots is not None else P
+    if out is None:
+        out = torch.empty_like(v)
+        if not out.is_contiguous():
+            out = torch.empty((T, Hv, dv), dtype=dt, device="cuda")
+    (qs, qh, qe), (ks, kh, ke), (vs, vh, ve) = q.stride(), k.stride(), v.stride()
+    f32 = torch.float32
+    if not (dt in _DTYPES and st in _DTYPES and k.dtype == dt and v.dtype == dt and out.dtype == dt and
+            g.dtype == f32 and beta.dtype == f32 and
+            k.shape == q.shape and v.shape[0] == T and out.shape == (T, Hv, dv) and
+            g.shape == ((T, Hv, dk) if channel else (T, Hv)) and beta.shape == (T, Hv) and
+            pool.shape == (P, Hv, dk, dv) and
+            (qe == 1 or dk == 1) and (ke == 1 or dk == 1) and (ve == 1 or dv == 1) and
+            (qh == dk or Hk == 1) and (kh == dk or Hk == 1) and (vh == dv or Hv == 1) and
+            g.is_contiguous() and beta.is_contiguous() and pool.is_contiguous() and
+            out.is_contiguous() and
+            _same_device(dev, k, v, g, beta, pool, slots, cu_seqlens, keep, reset, out, status) and
+            _index(slots, torch.int32, N) and _index(cu_seqlens, torch.int32, N + 1) and
+            _index(keep, torch.int32, N) and _index(reset, torch.bool, N) and
+            (status is None or status.nbytes >= 256)):
+        raise ValueError(
+            f"{name}: q, k [T,H_k,d_k], v [T,H_v,d_v] and out of one type (bf16 or fp32), heads of a "
+            "token next to each other; g [T,H_v] or [T,H_v,d_k] and beta [T,H_v] contiguous fp32; "
+            "pool [num_slots,H_v,d_k,d_v] contiguous, bf16 or fp32; slots, keep [N] and cu_seqlens "
+            "[N+1] int32, reset [N] bool; status of 256 bytes; all on one CUDA device")
+    if T <= 1:                    # the stride of one token is of no account
+        qs, ks, vs = max(qs, Hk * dk), max(ks, Hk * dk), max(vs, Hv * dv)
+    rc = lib().gdn_recurrent_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), pool.data_ptr(),
+        _at(slots), _at(cu_seqlens), _at(keep), _at(reset), N, T, Hk, Hv, dk, dv, P, qs, ks, vs,
+        channel, _DTYPES[dt], _DTYPES[st], out.data_ptr(), _at(status), _raw_stream(dev))
+    if rc != OK:
+        _check(rc, name)
     return out
 
 
-def _require(name, ok, what):
-    if not ok:
-        raise ValueError(f"{name}: {what}")
+_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _one_device(*ts):
-    ts = [t for t in ts if t is not None]
-    if not all(t.is_cuda and t.device == ts[0].device for t in ts):
-        raise ValueError("all tensors must be CUDA tensors on one device")
-    return ts[0].device
+@contextlib.contextmanager
+def _on(name, dev, stream):
+    """The tensors' device and the caller's stream as the current ones: outputs
+    are allocated on the stream that writes them."""
+    if dev < 0:
+        raise ValueError(f"{name}: all tensors must be CUDA tensors")
+    if stream is not None and stream.device_index != dev:
+        raise ValueError(f"{name}: the stream is on device {stream.device_index}, the tensors on {dev}")
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        yield
 
 
-def _token_stride(name, x):
-    """Elements between tokens; heads and channels lie next to each other."""
-    T, H, d = x.shape
-    _require(name, (d <= 1 or x.stride(2) == 1) and (H <= 1 or x.stride(1) == d),
-             "the heads of a token must be contiguous")
-    return x.stride(0) if T > 1 else max(x.stride(0), H * d)
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(dev, *ts):
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            return False
+    return dev >= 0
+
+
+def _index(t, dtype, n):
+    return t is None or (t.dtype == dtype and t.numel() == n and t.is_contiguous())
 
 
 # ---------------------------------------------------------------- queries and keys
@@ -448,66 +475,75 @@ class Packed(NamedTuple):
     scales: torch.Tensor
 
 
+def _rows_like(x, dtype):
+    if x is None:
+        return None
+    y = torch.empty_like(x) if x.dtype == dtype else torch.empty_like(x, dtype=dtype)
+    return y if y.is_contiguous() else torch.empty(x.shape, dtype=dtype, device="cuda")
+
+
 def _packed_empty(x):
     T, H, d = x.shape
-    return Packed(torch.empty(T, H, d, dtype=torch.float8_e4m3fn, device=x.device),
-                  torch.empty(T, H, (d + 31) // 32, dtype=torch.uint8, device=x.device))
+    return Packed(torch.empty((T, H, d), dtype=torch.float8_e4m3fn, device="cuda"),
+                  torch.empty((T, H, (d + 31) // 32), dtype=torch.uint8, device="cuda"))
 
 
-def _packed_arg(name, x):
+def _packed_arg(name, x, dev, shape=None):
     if x is None:
         return None
-    T, H, d = x[0].shape
-    _require(name, x[0].dtype == torch.float8_e4m3fn and x[1].dtype == torch.uint8 and
-             tuple(x[1].shape) == (T, H, (d + 31) // 32) and x[0].is_contiguous() and
-             x[1].is_contiguous(), "packed rows")
-    return _PackedRows(x[0].data_ptr(), x[1].data_ptr())
+    codes, scales = x
+    T, H, d = codes.shape
+    if not (codes.dtype == torch.float8_e4m3fn and scales.dtype == torch.uint8 and
+            scales.shape == (T, H, (d + 31) // 32) and codes.is_contiguous() and
+            scales.is_contiguous() and (shape is None or codes.shape == shape) and
+            codes.get_device() == dev and scales.get_device() == dev):
+        raise ValueError(f"{name}: packed rows are codes [T,H,d] float8_e4m3fn and scales "
+                         "[T,H,ceil(d/32)] uint8, contiguous, on one CUDA device")
+    return _PackedRows(codes.data_ptr(), scales.data_ptr())
 
 
-def _rows_arg(name, x, like=None, dtype=None):
+def _rows_arg(name, x, dev, shape, dtype):
     if x is None:
         return None
-    T, H, d = x.shape
-    _require(name, d <= 1 or x.stride(2) == 1, "the channels of a head must be contiguous")
-    _require(name, dtype is None or x.dtype == dtype, f"rows of {x.dtype} for {dtype}")
-    _require(name, like is None or tuple(x.shape) == tuple(like), "shapes of the rows")
-    hs = x.stride(1) if H > 1 else d
-    return _Rows(x.data_ptr(), x.stride(0) if T > 1 else (H - 1) * hs + d, hs)
+    (T, H, d), (ts, hs, es) = x.shape, x.stride()
+    if not (x.dtype == dtype and x.shape == shape and (es == 1 or d <= 1) and x.get_device() == dev):
+        raise ValueError(f"{name}: rows of shape {tuple(x.shape)} and {x.dtype}, expected "
+                         f"{tuple(shape)} and {dtype}, channels contiguous, on one CUDA device")
+    if H <= 1:
+        hs = d
+    return _Rows(x.data_ptr(), ts if T > 1 else (H - 1) * hs + d, hs)
 
 
-def _qk_params(name, q, k, dtype, w_q, w_k, positions, inv_freq, norm, eps, interleaved,
+def _qk_params(name, dev, qs, ks, dtype, w_q, w_k, positions, inv_freq, norm, eps, interleaved,
                weight_offset, q_scale, rope_scale):
-    T, Hq, d = (q if q is not None else k).shape
-    Hk = 0 if k is None else k.shape[1]
-    _require(name, k is None or (k.shape[0] == T and k.shape[2] == d), "q and k shapes")
-    _require(name, norm in _NORMS, f"norm is one of {sorted(_NORMS)}")
-    _require(name, (positions is None) == (inv_freq is None), "positions come with inv_freq")
-    rot = 0
-    if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        _require(name, rot <= d, "inv_freq has more than d / 2 values")
-        _require(name, inv_freq.dtype == torch.float64 and inv_freq.is_contiguous(),
-                 "inv_freq is contiguous fp64")
-        _require(name, positions.dtype == torch.int32 and positions.is_contiguous() and
-                 positions.numel() == T, "positions are contiguous int32, one a token")
-    for w in (w_q, w_k):
-        _require(name, w is None or (w.dtype == dtype and w.numel() == d and w.is_contiguous()),
-                 "weights are contiguous [d] of the rows' dtype")
-    _require(name, k is not None or w_k is None, "w_k without k")
-    return _QkParams(T, Hq if q is not None else 0, Hk, d, rot, int(interleaved), _NORMS[norm],
-                     _dtype_code(dtype), eps, weight_offset, q_scale, rope_scale,
-                     None if rot == 0 else positions.data_ptr(),
-                     None if rot == 0 else inv_freq.data_ptr(),
-                     None if w_q is None else w_q.data_ptr(),
-                     None if w_k is None else w_k.data_ptr())
+    """qs, ks: shapes of q and k (ks None without k)."""
+    T, Hq, d = qs
+    Hk = 0 if ks is None else ks[1]
+    if not (dtype in _DTYPES and norm in _NORMS and (ks is None or (ks[0] == T and ks[2] == d)) and
+            (positions is None) == (inv_freq is None) and (ks is not None or w_k is None)):
+        raise ValueError(f"{name}: q and k [T,H,d] of bf16 or fp32, norm one of {sorted(_NORMS)}, "
+                         "positions together with inv_freq, w_k only with k")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if not (_index(positions, torch.int32, T) and (rot == 0 or (
+            rot <= d and _index(inv_freq, torch.float64, rot // 2))) and
+            _index(w_q, dtype, d) and _index(w_k, dtype, d) and
+            _same_device(dev, positions, inv_freq, w_q, w_k)):
+        raise ValueError(f"{name}: positions int32 [T], inv_freq float64 [rot/2] with rot <= d, w_q "
+                         "and w_k [d] of the rows' dtype, contiguous, on one CUDA device")
+    return _QkParams(T, Hq, Hk, d, rot, interleaved, _NORMS[norm], _DTYPES[dtype], eps, weight_offset,
+                     q_scale, rope_scale, _at(positions) if rot else None,
+                     _at(inv_freq) if rot else None, _at(w_q), _at(w_k))
 
 
-def _ref(x):
-    return None if x is None else ctypes.byref(x)
-
-
-def _is_packed(x):
-    return isinstance(x, tuple)
+def _qk_source(name, q, k):
+    """(packed?, the tensor whose shape is q's, k's or None)."""
+    if isinstance(q, tuple):
+        if k is not None and not isinstance(k, tuple):
+            raise ValueError(f"{name}: q and k both packed, or neither")
+        return True, q[0], None if k is None else k[0]
+    if isinstance(k, tuple):
+        raise ValueError(f"{name}: q and k both packed, or neither")
+    return False, q, k
 
 
 def qk_norm_rope_fwd(q, k, w_q=None, w_k=None, positions=None, inv_freq=None, norm="l2", eps=1e-6,
@@ -523,36 +559,41 @@ def qk_norm_rope_fwd(q, k, w_q=None, w_k=None, positions=None, inv_freq=None, no
     rows' dtype) or None, to which weight_offset is added; inv_freq: fp64
     [rot/2] and positions: int32 [T] rotate the first rot elements, by halves
     or interleaved pairs, times rope_scale; q_scale multiplies q's outputs.
-    out: ``(q_out, k_out)`` to write to; an output may be its own input."""
+    out: ``(q_out, k_out)`` to write to; an output may be its own input, and
+    with pack=True None, to write the 8-bit rows alone."""
     name = "gdn_qk_norm_rope_fwd"
-    packed = _is_packed(q)
-    _require(name, k is None or _is_packed(k) == packed, "q and k both packed, or neither")
-    _require(name, not (packed and pack), "the rows are packed already")
-    qx, kx = (q[0], k and k[0]) if packed else (q, k)
-    extra = (*q, *(k or ())) if packed else (q, k)
-    dev = _one_device(*extra, w_q, w_k, positions, inv_freq, *(out or ()))
-    dtype = (dtype or torch.bfloat16) if packed else qx.dtype
-    p = _qk_params(name, qx, kx, dtype, w_q, w_k, positions, inv_freq, norm, eps, interleaved,
+    packed, qx, kx = _qk_source(name, q, k)
+    dev = qx.get_device()
+    if dev < 0 or stream is not None or dev != torch.cuda.current_device():
+        with _on(name, dev, stream):
+            return qk_norm_rope_fwd(q, k, w_q, w_k, positions, inv_freq, norm, eps, interleaved,
+                                    weight_offset, q_scale, rope_scale, pack, dtype, out)
+    if packed:
+        if pack:
+            raise ValueError(f"{name}: the rows are packed already")
+        dtype = dtype or torch.bfloat16
+    else:
+        dtype = qx.dtype
+    qs, ks = qx.shape, None if kx is None else kx.shape
+    p = _qk_params(name, dev, qs, ks, dtype, w_q, w_k, positions, inv_freq, norm, eps, interleaved,
                    weight_offset, q_scale, rope_scale)
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
-        if out is None:
-            out = tuple(None if x is None else torch.empty(x.shape, dtype=dtype, device=dev)
-                        for x in (qx, kx))
-        outs = [_rows_arg(name, o, None if x is None else x.shape, dtype)
-                for o, x in zip(out, (qx, kx))]
-        if packed:
-            rc = lib().gdn_qk_norm_rope_fwd_packed(
-                ctypes.byref(p), _ref(_packed_arg(name, q)), _ref(_packed_arg(name, k)),
-                _ref(outs[0]), _ref(outs[1]), _stream_ptr(stream))
+    qo, ko = out if out is not None else (_rows_like(qx, dtype), _rows_like(kx, dtype))
+    qr, kr = _rows_arg(name, qo, dev, qs, dtype), _rows_arg(name, ko, dev, ks, dtype)
+    s = _raw_stream(dev)
+    if packed:
+        rc = lib().gdn_qk_norm_rope_fwd_packed(p, _packed_arg(name, q, dev), _packed_arg(name, k, dev),
+                                               qr, kr, s)
+        if rc != OK:
             _check(rc, name + "_packed")
-            return tuple(out)
-        q8, k8 = (None if x is None or not pack else _packed_empty(x) for x in (q, k))
-        rc = lib().gdn_qk_norm_rope_fwd(
-            ctypes.byref(p), _ref(_rows_arg(name, q)), _ref(_rows_arg(name, k, None, dtype)),
-            _ref(outs[0]), _ref(outs[1]), _ref(_packed_arg(name, q8)), _ref(_packed_arg(name, k8)),
-            _stream_ptr(stream))
-    _check(rc, name)
-    return (*out, q8, k8) if pack else tuple(out)
+        return qo, ko
+    q8 = _packed_empty(q) if pack else None
+    k8 = _packed_empty(k) if pack and k is not None else None
+    rc = lib().gdn_qk_norm_rope_fwd(p, _rows_arg(name, q, dev, qs, dtype),
+                                    _rows_arg(name, k, dev, ks, dtype), qr, kr,
+                                    _packed_arg(name, q8, dev), _packed_arg(name, k8, dev), s)
+    if rc != OK:
+        _check(rc, name)
+    return (qo, ko, q8, k8) if pack else (qo, ko)
 
 
 def qk_norm_rope_bwd(dq_out, dk_out, q, k, w_q=None, w_k=None, positions=None, inv_freq=None,
@@ -564,36 +605,45 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, w_q=None, w_k=None, positions=None, i
     dq, dk (the rows' dtype; for packed rows ``dtype``, bfloat16 if not given),
     dw_q, dw_k ([d] fp32, None without weights). out: ``(dq, dk)`` to write."""
     name = "gdn_qk_norm_rope_bwd"
-    packed = _is_packed(q)
-    _require(name, k is None or _is_packed(k) == packed, "q and k both packed, or neither")
-    qx, kx = (q[0], k and k[0]) if packed else (q, k)
-    extra = (*q, *(k or ())) if packed else (q, k)
-    dev = _one_device(*extra, dq_out, dk_out, w_q, w_k, positions, inv_freq, *(out or ()))
+    packed, qx, kx = _qk_source(name, q, k)
+    dev = qx.get_device()
+    if dev < 0 or stream is not None or dev != torch.cuda.current_device():
+        with _on(name, dev, stream):
+            return qk_norm_rope_bwd(dq_out, dk_out, q, k, w_q, w_k, positions, inv_freq, norm, eps,
+                                    interleaved, weight_offset, q_scale, rope_scale, dtype, out,
+                                    workspace)
     dtype = (dtype or torch.bfloat16) if packed else qx.dtype
-    p = _qk_params(name, qx, kx, dtype, w_q, w_k, positions, inv_freq, norm, eps, interleaved,
+    qs, ks = qx.shape, None if kx is None else kx.shape
+    p = _qk_params(name, dev, qs, ks, dtype, w_q, w_k, positions, inv_freq, norm, eps, interleaved,
                    weight_offset, q_scale, rope_scale)
-    grads = [_rows_arg(name, g, None if x is None else x.shape, dq_out.dtype)
-             for g, x in zip((dq_out, dk_out), (qx, kx))]
-    _require(name, kx is None or dk_out is not None, "dk_out")
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
-        if out is None:
-            out = tuple(None if x is None else torch.empty(x.shape, dtype=dtype, device=dev)
-                        for x in (qx, kx))
-        outs = [_rows_arg(name, o, None if x is None else x.shape, dtype)
-                for o, x in zip(out, (qx, kx))]
-        dw = [None if w is None else torch.empty(w.numel(), dtype=torch.float32, device=dev)
-              for w in (w_q, w_k)]
-        need = int(lib().gdn_qk_norm_rope_bwd_workspace_size(ctypes.byref(p)))
-        if need and (workspace is None or workspace.numel() < need):
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        src = ([_packed_arg(name, q), _packed_arg(name, k)] if packed else
-               [_rows_arg(name, q), _rows_arg(name, k, None, dtype)])
-        fn = lib().gdn_qk_norm_rope_bwd_packed if packed else lib().gdn_qk_norm_rope_bwd
-        rc = fn(ctypes.byref(p), _ref(grads[0]), _ref(grads[1]), _dtype_code(dq_out.dtype),
-                _ref(src[0]), _ref(src[1]), _ref(outs[0]), _ref(outs[1]), _ptr(dw[0]), _ptr(dw[1]),
-                _ptr(workspace), need, _stream_ptr(stream))
-    _check(rc, name + ("_packed" if packed else ""))
-    return dict(dq=out[0], dk=out[1], dw_q=dw[0], dw_k=dw[1])
+    gt = dq_out.dtype
+    if gt not in _DTYPES or (ks is None) != (dk_out is None):
+        raise ValueError(f"{name}: dq_out, dk_out like the outputs, fp32 or the rows' dtype")
+    dyq, dyk = _rows_arg(name, dq_out, dev, qs, gt), _rows_arg(name, dk_out, dev, ks, gt)
+    dq, dk = out if out is not None else (_rows_like(qx, dtype), _rows_like(kx, dtype))
+    d = qs[2]
+    dwq = None if w_q is None else torch.empty(d, dtype=torch.float32, device="cuda")
+    dwk = None if w_k is None else torch.empty(d, dtype=torch.float32, device="cuda")
+    need = 0
+    if dwq is not None or dwk is not None:
+        need = lib().gdn_qk_norm_rope_bwd_workspace_size(p)
+        if workspace is None or workspace.nbytes < need:
+            workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+        elif workspace.get_device() != dev:
+            raise ValueError(f"{name}: workspace on another device")
+    qr, kr = _rows_arg(name, dq, dev, qs, dtype), _rows_arg(name, dk, dev, ks, dtype)
+    s = _raw_stream(dev)
+    if packed:
+        rc = lib().gdn_qk_norm_rope_bwd_packed(
+            p, dyq, dyk, _DTYPES[gt], _packed_arg(name, q, dev), _packed_arg(name, k, dev), qr, kr,
+            _at(dwq), _at(dwk), _at(workspace), need, s)
+    else:
+        rc = lib().gdn_qk_norm_rope_bwd(
+            p, dyq, dyk, _DTYPES[gt], _rows_arg(name, q, dev, qs, dtype),
+            _rows_arg(name, k, dev, ks, dtype), qr, kr, _at(dwq), _at(dwk), _at(workspace), need, s)
+    if rc != OK:
+        _check(rc, name + ("_packed" if packed else ""))
+    return dict(dq=dq, dk=dk, dw_q=dwq, dw_k=dwk)
 
 
 def pack(x, stream=None) -> Packed:
