@@ -7,13 +7,13 @@
 //   x_i = sum_j st[j][i] a_j k_j,  u_i = beta (v_i - x_i)
 //   st[j][i] <- a_j st[j][i] + u_i k_j,  o_i = sum_j st[j][i] q_j
 //
-// Up to four tokens are taken together, so that a pass over the state serves
-// all of them and the chain from token to token runs over a few scalars. With
-// S the state before the block, c_m = a_0 .. a_m, d_ml = a_(l+1) .. a_m:
+// Two tokens are taken together, so that a pass over the state serves both and
+// the chain from token to token runs over a few scalars. With S the state
+// before the two, c_m = a_0 .. a_m:
 //   X_m = S^T k_m,  Y_m = S^T q_m                    (one pass, one reduction)
-//   u_m = beta_m (v_m - c_m X_m - sum_(l<m) d_ml (k_l . k_m) u_l)
-//   o_m = c_m Y_m + sum_(l<=m) d_ml (k_l . q_m) u_l
-//   S  <- c_last S + sum_l d_(last,l) u_l k_l         (one pass)
+//   u_0 = beta_0 (v_0 - c_0 X_0),  u_1 = beta_1 (v_1 - c_1 X_1 - a_1 (k_0 . k_1) u_0)
+//   o_0 = c_0 Y_0 + (k_0 . q_0) u_0,  o_1 = c_1 Y_1 + a_1 (k_0 . q_1) u_0 + (k_1 . q_1) u_1
+//   S  <- c_1 S + a_1 u_0 k_0 + u_1 k_1              (one pass)
 // With the channel gate the products of decays sit inside the dot products and
 // in rows of k and q scaled by them. All of them are products of the tokens'
 // own decays, never quotients, so a decay of zero is as good as any other.
@@ -26,9 +26,15 @@
 // reduced over the eight rg lanes by halving (7 shuffles a token), after which
 // one lane holds a column's X of every token and its neighbour the Y.
 //
-// k, q, v and the decays come through shared memory in fp32, a token a warp:
-// the rows of block n + 2 are on their way from HBM, those of block n + 1 are
-// multiplied with each other, while block n is computed.
+// (Four together take no fewer multiply-adds a token and half as many steps,
+// but 64 more registers and twice the code: 63 us against 47 us for 64 runs of
+// one to six tokens of 32 heads.)
+//
+// k, q, v and the decays of up to four tokens at a time come through shared
+// memory in fp32, a token a warp: the rows of the group after next are on their
+// way from HBM, those of the next are multiplied with each other, while this
+// one is computed. k and q lie there twice over, k_j k_j, so that one 16-byte
+// read gives the operands of paired multiply-adds for two rows.
 #include "gdn_internal.cuh"
 #include "rows.cuh"
 
@@ -36,7 +42,7 @@ namespace gdn {
 namespace {
 
 constexpr int kRecWarps = 4, kRecCols = 16 * kRecWarps;   // columns of d_v per CTA
-constexpr int kBlock = 4;                                 // tokens taken together
+constexpr int kGroup = 4;                                 // tokens staged together
 
 struct RecArgs {
   const void *q, *k, *v;
@@ -52,32 +58,34 @@ struct RecArgs {
   bool vec;                         // q, k, v rows can be read four elements at a time
 };
 
-// A block's tokens as they came, in fp32. Tokens past the block's end are zero
+// A group's tokens as they came, in fp32. Tokens past the group's end are zero
 // with decay 1.
 template <bool KDA>
 struct alignas(16) RecRows {
-  float k[kBlock][128], q[kBlock][128], v[kBlock][kRecCols];
-  float a[kBlock][KDA ? 128 : 4];
-  float beta[kBlock];
+  float k[kGroup][128], q[kGroup][128];
+  float a[kGroup][KDA ? 128 : 4];
+  float beta[kGroup];
 };
-// What follows from them.
+// What the passes over the state take: rows twice over, and for each pair of
+// tokens m = 0, 1 the scalars.
 template <bool KDA>
 struct alignas(16) RecCoef {
-  float A[kBlock][kBlock], P[kBlock][kBlock];   // [m][l]: d_ml (k_l . k_m), d_ml (k_l . q_m)
-  float c[kBlock], e[kBlock];                   // c_m and d_(last, l); 1 with the channel gate
-  float ka[KDA ? kBlock : 1][128], qa[KDA ? kBlock : 1][128];   // c_m k_m, c_m q_m per channel
-  float ke[KDA ? kBlock : 1][128], ce[KDA ? 128 : 1];           // d_(last, l) k_l, c_last
+  float2 kx[kGroup][128], qx[kGroup][128];   // k and q (channel gate: c_m k_m, c_m q_m)
+  float2 ku[KDA ? kGroup : 1][128];          // channel gate: the second of the two's decay times k_m
+  float2 cu[KDA ? kGroup / 2 : 1][128];      // channel gate: c of the two, per row
+  float4 s[kGroup];                          // c_m, beta_m, then d k_0 . k_1 and k_m . q_m
+  float dq[kGroup], e[kGroup];               // d k_0 . q_1 (second tokens); decay after m in the two
 };
 template <bool KDA>
 struct alignas(16) RecShared {
-  RecRows<KDA> rows[3];
-  RecCoef<KDA> coef[2];
-  float u[kRecWarps][kBlock][16];
+  RecRows<KDA> rows[2];              // of the next group; being fetched for the one after
+  RecCoef<KDA> coef[2];              // of this group and of the next
+  float v[3][kGroup][kRecCols];      // of all three
+  float u[kRecWarps][2][16];
 };
-
 static_assert(sizeof(RecRows<false>) % 16 == 0 && sizeof(RecRows<true>) % 16 == 0 &&
               sizeof(RecCoef<false>) % 16 == 0 && sizeof(RecCoef<true>) % 16 == 0 &&
-              offsetof(RecCoef<false>, ka) % 16 == 0 && offsetof(RecRows<false>, a) % 16 == 0,
+              offsetof(RecCoef<false>, s) % 16 == 0 && offsetof(RecRows<false>, a) % 16 == 0,
               "rows are read in 16-byte pieces");
 
 template <typename T>
@@ -103,150 +111,142 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) {
 __device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ void sts4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
 
-// One token's share of a lane.
-template <bool KDA>
-struct RecToken {
-  float4 k, q, v, a;
-  float beta;
-};
+__device__ __forceinline__ void copy_async(void *to, const void *from, int bytes) {
+  const uint32_t p = uint32_t(__cvta_generic_to_shared(to));
+  if (bytes == 16) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(p), "l"(from) : "memory");
+  else if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(p), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(p), "l"(from) : "memory");
+}
 
+// Starts the copy of token t's rows, as they are, to where land() turns them
+// into fp32 in place; rows that cannot be copied in pieces are read here.
 template <typename T, bool KDA>
-__device__ __forceinline__ void fetch(const RecArgs &A, int64_t t, bool on, int h, int hk, int col0,
-                                      int lane, RecToken<KDA> &r) {
+__device__ __forceinline__ void fetch(const RecArgs &A, int64_t t, int h, int hk, int col0, int lane,
+                                      RecRows<KDA> &R, float (*v)[kRecCols], int m) {
   const int c = lane * 4;
-  r.k = r.q = r.v = make_float4(0.f, 0.f, 0.f, 0.f);
-  r.a = make_float4(1.f, 1.f, 1.f, 1.f);
-  r.beta = 0.f;
-  if (!on) return;
-  r.k = load4(static_cast<const T *>(A.k) + t * A.k_stride + int64_t(hk) * A.dk + c, A.dk - c, A.vec);
-  r.q = load4(static_cast<const T *>(A.q) + t * A.q_stride + int64_t(hk) * A.dk + c, A.dk - c, A.vec);
-  if (c < kRecCols)
-    r.v = load4(static_cast<const T *>(A.v) + t * A.v_stride + int64_t(h) * A.dv + col0 + c,
-                A.dv - col0 - c, A.vec);
-  if (KDA) {
-    const float *gp = A.g + (t * A.Hv + h) * A.dk + c;
-    if (c + 0 < A.dk) r.a.x = gp[0];
-    if (c + 1 < A.dk) r.a.y = gp[1];
-    if (c + 2 < A.dk) r.a.z = gp[2];
-    if (c + 3 < A.dk) r.a.w = gp[3];
-  } else {
-    r.a.x = A.g[t * A.Hv + h];
-  }
-  r.beta = A.beta[t * A.Hv + h];
-}
-
-template <bool KDA>
-__device__ __forceinline__ void put(RecRows<KDA> &R, int m, bool on, int lane, int dk,
-                                    const RecToken<KDA> &r) {
-  const int c = lane * 4;
-  sts4(&R.k[m][c], r.k);
-  sts4(&R.q[m][c], r.q);
-  if (c < kRecCols) sts4(&R.v[m][c], r.v);
-  if (KDA) {
-    float4 a = r.a;
-    if (on) {
-      a.x = c + 0 < dk ? expf(a.x) : 1.f;
-      a.y = c + 1 < dk ? expf(a.y) : 1.f;
-      a.z = c + 2 < dk ? expf(a.z) : 1.f;
-      a.w = c + 3 < dk ? expf(a.w) : 1.f;
+  const T *kp = static_cast<const T *>(A.k) + t * A.k_stride + int64_t(hk) * A.dk + c;
+  const T *qp = static_cast<const T *>(A.q) + t * A.q_stride + int64_t(hk) * A.dk + c;
+  const T *vp = static_cast<const T *>(A.v) + t * A.v_stride + int64_t(h) * A.dv + col0 + c;
+  const float *gp = A.g + (t * A.Hv + h) * (KDA ? A.dk : 1);
+  if (A.vec) {
+    if (c < A.dk) {
+      copy_async(reinterpret_cast<T *>(R.k[m]) + c, kp, 4 * sizeof(T));
+      copy_async(reinterpret_cast<T *>(R.q[m]) + c, qp, 4 * sizeof(T));
+      if (KDA) copy_async(&R.a[m][c], gp + c, 16);
     }
-    sts4(&R.a[m][c], a);
-  } else if (lane == 0) {
-    R.a[m][0] = on ? expf(r.a.x) : 1.f;
+    if (c < kRecCols && col0 + c < A.dv) copy_async(reinterpret_cast<T *>(v[m]) + c, vp, 4 * sizeof(T));
+  } else {
+    sts4(&R.k[m][c], load4(kp, A.dk - c, false));
+    sts4(&R.q[m][c], load4(qp, A.dk - c, false));
+    if (KDA) sts4(&R.a[m][c], load4(gp + c, A.dk - c, false));
+    if (c < kRecCols) sts4(&v[m][c], load4(vp, A.dv - col0 - c, false));
   }
-  if (lane == 0) R.beta[m] = r.beta;
+  if (lane == 0) {
+    if (!KDA) copy_async(&R.a[m][0], gp, 4);
+    copy_async(&R.beta[m], A.beta + t * A.Hv + h, 4);
+  }
 }
 
-// Warp m works out what token m has to do with those before it.
+template <typename T>
+__device__ __forceinline__ float4 landed(const float *row, int lane, bool there, bool raw) {
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!there) return zero;
+  return raw ? ld4(reinterpret_cast<const T *>(row) + 4 * lane) : lds4(row + 4 * lane);
+}
+template <typename T, bool KDA>
+__device__ __forceinline__ void land(const RecArgs &A, bool on, int col0, int lane, RecRows<KDA> &R,
+                                     float (*v)[kRecCols], int m) {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  const int c = lane * 4;
+  const bool vc = c < kRecCols && col0 + c < A.dv;
+  const float4 k4 = landed<T>(R.k[m], lane, on && c < A.dk, A.vec);
+  const float4 q4 = landed<T>(R.q[m], lane, on && c < A.dk, A.vec);
+  const float4 v4 = landed<T>(v[m], lane, on && vc, A.vec);
+  float4 a4 = make_float4(1.f, 1.f, 1.f, 1.f);
+  if (KDA && on && c < A.dk) {
+    const float4 g = lds4(&R.a[m][c]);
+    a4.x = expf(g.x);
+    if (c + 1 < A.dk) a4.y = expf(g.y);
+    if (c + 2 < A.dk) a4.z = expf(g.z);
+    if (c + 3 < A.dk) a4.w = expf(g.w);
+  }
+  __syncwarp();                       // everything is read before anything is overwritten
+  sts4(&R.k[m][c], k4);
+  sts4(&R.q[m][c], q4);
+  if (c < kRecCols) sts4(&v[m][c], v4);
+  if (KDA) sts4(&R.a[m][c], a4);
+  if (lane == 0) {
+    if (!KDA) R.a[m][0] = on ? expf(R.a[m][0]) : 1.f;
+    if (!on) R.beta[m] = 0.f;
+  }
+}
+
+__device__ __forceinline__ void put_twice(float2 *p, float4 x) {
+  *reinterpret_cast<float4 *>(p) = make_float4(x.x, x.x, x.y, x.y);
+  *reinterpret_cast<float4 *>(p + 2) = make_float4(x.z, x.z, x.w, x.w);
+}
+
+// Warp m works out what token m has to do with the one before it. nb: tokens of
+// the group.
 template <bool KDA>
 __device__ __forceinline__ void relate(const RecRows<KDA> &R, RecCoef<KDA> &C, int m, int nb, int lane) {
-  const int c = lane * 4;
-  if (m >= nb) {
-    if (KDA) {      // a token of padding multiplies these by zero
-      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-      sts4(&C.ka[m][c], zero);
-      sts4(&C.qa[m][c], zero);
-      sts4(&C.ke[m][c], zero);
-    }
-    return;
-  }
-  const float4 km = lds4(&R.k[m][c]), qm = lds4(&R.q[m][c]);
-  float z[8];                         // k_l . k_m (l = 0..3), k_l . q_m
-  float4 kd = km, qd = qm;            // with the decays since l
-#pragma unroll
-  for (int l = kBlock - 1; l >= 0; --l) {
-    z[l] = z[4 + l] = 0.f;
-    if (l > m) continue;
-    const float4 kl = lds4(&R.k[l][c]);
-    if (KDA && l < m) {
-      const float4 a = lds4(&R.a[l + 1][c]);
-      kd = mul4(kd, a);
-      qd = mul4(qd, a);
-    }
-    z[l] = dot4(kl, kd);
-    z[4 + l] = dot4(kl, qd);
-  }
+  const int c = lane * 4, f = m & ~1;                 // f: the first of the two
+  if (f >= nb) return;
+  const bool second = m & 1;
+  const float4 km = lds4(&R.k[m][c]), qm = lds4(&R.q[m][c]), kf = lds4(&R.k[f][c]);
+  float4 kd = km, qd = qm;                            // with the decay since the first
+  float am = 1.f, a0 = 1.f, a1 = 1.f;
   if (KDA) {
-    const float4 a0 = lds4(&R.a[0][c]);
-    sts4(&C.ka[m][c], mul4(kd, a0));
-    sts4(&C.qa[m][c], mul4(qd, a0));
-    float4 e = make_float4(1.f, 1.f, 1.f, 1.f);
-    for (int l = m + 1; l < nb; ++l) e = mul4(e, lds4(&R.a[l][c]));
-    sts4(&C.ke[m][c], mul4(km, e));
-    if (m == 0) sts4(&C.ce[c], mul4(a0, e));
-  }
-  // sum over the warp by halving: lane bits 4, 3, 2 pick one of the eight
-  float y4[4], y2[2], y;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    y4[i] = (lane & 16 ? z[4 + i] : z[i]) + __shfl_xor_sync(~0u, lane & 16 ? z[i] : z[4 + i], 16);
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    y2[i] = (lane & 8 ? y4[2 + i] : y4[i]) + __shfl_xor_sync(~0u, lane & 8 ? y4[i] : y4[2 + i], 8);
-  y = (lane & 4 ? y2[1] : y2[0]) + __shfl_xor_sync(~0u, lane & 4 ? y2[0] : y2[1], 4);
-  y += __shfl_xor_sync(~0u, y, 2);
-  y += __shfl_xor_sync(~0u, y, 1);
-  const int l = (lane >> 2) & 3;
-  float d = 1.f, cm = 1.f, e = 1.f;
-  if (!KDA) {
-#pragma unroll
-    for (int i = 0; i < kBlock; ++i) {
-      const float a = R.a[i][0];
-      if (i <= m) cm *= a;
-      if (i <= m && i > l) d *= a;
-      if (i > m && i < nb) e *= a;
+    const float4 a = lds4(&R.a[m][c]);
+    float4 x = a;                                     // c_m
+    if (second) {
+      kd = mul4(km, a);
+      qd = mul4(qm, a);
+      x = mul4(a, lds4(&R.a[f][c]));
     }
+    put_twice(&C.kx[m][c], mul4(km, x));
+    put_twice(&C.qx[m][c], mul4(qm, x));
+    put_twice(&C.ku[m][c], second ? km : mul4(km, lds4(&R.a[f + 1][c])));
+    if (second) put_twice(&C.cu[f / 2][c], x);
+  } else {
+    put_twice(&C.kx[m][c], km);
+    put_twice(&C.qx[m][c], qm);
+    a0 = R.a[f][0];
+    a1 = R.a[f + 1][0];
+    am = a1;
   }
-  if ((lane & 3) == 0) (lane & 16 ? C.P : C.A)[m][l] = d * y;
-  if (lane == 0) { C.c[m] = cm; C.e[m] = e; }
+  const float kk = warp_sum(second ? dot4(kf, kd) : 0.f), kq = warp_sum(dot4(km, qm));
+  const float dq = warp_sum(second ? dot4(kf, qd) : 0.f);
+  if (lane == 0) {
+    C.s[m] = make_float4(KDA ? 1.f : second ? a0 * a1 : a0, R.beta[m], am * kk, kq);
+    C.dq[m] = am * dq;
+    C.e[m] = second ? 1.f : a1;
+  }
 }
 
-// One block of B tokens (the last may be padding) on a warp's columns.
+// The tokens f, f + 1 of a group (B = 1: f alone) on a warp's columns; update:
+// whether the state after them is wanted.
 template <typename T, bool KDA, int NP, int B>
-__device__ __forceinline__ void block_step(const RecRows<KDA> &R, const RecCoef<KDA> &C, float (*us)[16],
-                                           float4 (&S)[NP * 4], int nb, int lane, int wcol, T *o,
-                                           int64_t o_stride, bool col_ok) {
+__device__ __forceinline__ void step(const float (*v)[kRecCols], const RecCoef<KDA> &C, int f, float (*us)[16],
+                                     Pair (&S)[NP * 4][2], int lane, int wcol, T *o, int64_t o_stride,
+                                     bool col_ok, bool update) {
   const int rg = lane >> 2, cg = lane & 3;
-  float xy[2 * B][4];                 // X_0.., Y_0.. of four columns, this lane's rows
+  Pair xy[2 * B][2];                  // X_0.., Y_0.. of two pairs of columns, this lane's rows
 #pragma unroll
-  for (int m = 0; m < 2 * B; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) xy[m][i] = 0.f;
+  for (int m = 0; m < 2 * B; ++m) xy[m][0] = xy[m][1] = pair(0.f, 0.f);
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
 #pragma unroll
-    for (int m = 0; m < B; ++m) {
-      const int at = 32 * p + 4 * rg;
-      const float4 k4 = lds4(KDA ? &C.ka[m][at] : &R.k[m][at]);
-      const float4 q4 = lds4(KDA ? &C.qa[m][at] : &R.q[m][at]);
-      const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
+    for (int m = 0; m < 2 * B; ++m) {
+      const float2 *row = (m < B ? C.kx[f + m] : C.qx[f + m - B]) + 32 * p + 4 * rg;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float4 s = S[4 * p + r];
-        xy[m][0] += s.x * kk[r]; xy[m][1] += s.y * kk[r];
-        xy[m][2] += s.z * kk[r]; xy[m][3] += s.w * kk[r];
-        xy[B + m][0] += s.x * qq[r]; xy[B + m][1] += s.y * qq[r];
-        xy[B + m][2] += s.z * qq[r]; xy[B + m][3] += s.w * qq[r];
+      for (int r = 0; r < 4; r += 2) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(row + r);
+        xy[m][0] = fma2(S[4 * p + r][0], w.x, xy[m][0]);
+        xy[m][1] = fma2(S[4 * p + r][1], w.x, xy[m][1]);
+        xy[m][0] = fma2(S[4 * p + r + 1][0], w.y, xy[m][0]);
+        xy[m][1] = fma2(S[4 * p + r + 1][1], w.y, xy[m][1]);
       }
     }
   }
@@ -255,70 +255,86 @@ __device__ __forceinline__ void block_step(const RecRows<KDA> &R, const RecCoef<
   float t1[2 * B], z[B];
 #pragma unroll
   for (int m = 0; m < 2 * B; ++m) {
-    const float lo = (b4 ? xy[m][2] : xy[m][0]) + __shfl_xor_sync(~0u, b4 ? xy[m][0] : xy[m][2], 16);
-    const float hi = (b4 ? xy[m][3] : xy[m][1]) + __shfl_xor_sync(~0u, b4 ? xy[m][1] : xy[m][3], 16);
+    const float2 lo2 = unpair(b4 ? xy[m][1] : xy[m][0]), give = unpair(b4 ? xy[m][0] : xy[m][1]);
+    const float lo = lo2.x + __shfl_xor_sync(~0u, give.x, 16);
+    const float hi = lo2.y + __shfl_xor_sync(~0u, give.y, 16);
     t1[m] = (b3 ? hi : lo) + __shfl_xor_sync(~0u, b3 ? lo : hi, 8);
   }
 #pragma unroll
   for (int m = 0; m < B; ++m)
     z[m] = (b2 ? t1[B + m] : t1[m]) + __shfl_xor_sync(~0u, b2 ? t1[m] : t1[B + m], 4);
   const int c = cg * 4 + (b4 ? 2 : 0) + (b3 ? 1 : 0);     // this lane's column of the warp's 16
-  float u[B];
-#pragma unroll
-  for (int m = 0; m < B; ++m) {       // right in the X lanes; the Y lanes take it from there
-    float x = R.v[m][wcol + c] - (KDA ? z[m] : C.c[m] * z[m]);
-#pragma unroll
-    for (int l = 0; l < m; ++l) x -= C.A[m][l] * u[l];
-    u[m] = m < nb ? R.beta[m] * x : 0.f;
+  // u in the X lanes; the Y lanes take it from there
+  const float4 s0 = C.s[f], s1 = C.s[f + B - 1];
+  const float z0 = KDA ? z[0] : s0.x * z[0], z1 = KDA ? z[B - 1] : s1.x * z[B - 1];
+  const float u0x = s0.y * (v[f][wcol + c] - z0);
+  const float u1x = B == 2 ? s1.y * (v[f + 1][wcol + c] - z1 - s1.z * u0x) : 0.f;
+  const float u0o = __shfl_xor_sync(~0u, u0x, 4), u1o = B == 2 ? __shfl_xor_sync(~0u, u1x, 4) : 0.f;
+  if (b2) {
+    if (col_ok) {
+      o[c] = from_f32<T>(z0 + s0.w * u0o);
+      if (B == 2) o[o_stride + c] = from_f32<T>(z1 + C.dq[f + 1] * u0o + s1.w * u1o);
+    }
+  } else {
+    us[0][c] = B == 2 && !KDA ? C.e[f] * u0x : u0x;
+    if (B == 2) us[1][c] = u1x;
   }
   __syncwarp();
-  if (!b2)
-#pragma unroll
-    for (int m = 0; m < B; ++m) us[m][c] = KDA || m >= nb ? u[m] : C.e[m] * u[m];
+  if (!update) return;
+  Pair w[B][2];
 #pragma unroll
   for (int m = 0; m < B; ++m) {
-    const float other = __shfl_xor_sync(~0u, u[m], 4);
-    u[m] = b2 ? other : u[m];
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&us[m][4 * cg]);
+    w[m][0] = x.x;
+    w[m][1] = x.y;
   }
-  __syncwarp();
-  if (b2 && col_ok)
-#pragma unroll
-    for (int m = 0; m < B; ++m)
-      if (m < nb) {
-        float y = KDA ? z[m] : C.c[m] * z[m];
-#pragma unroll
-        for (int l = 0; l <= m; ++l) y += C.P[m][l] * u[l];
-        o[m * o_stride + c] = from_f32<T>(y);
-      }
-  float4 w[B];
-#pragma unroll
-  for (int m = 0; m < B; ++m) w[m] = lds4(&us[m][4 * cg]);
-  const float cl = KDA ? 1.f : C.c[nb - 1];
+  __syncwarp();                       // read before the next pair's are written
+  const Pair cl = pair(s1.x, s1.x);
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     const int at = 32 * p + 4 * rg;
-    float4 a4 = make_float4(cl, cl, cl, cl);
-    if (KDA) a4 = lds4(&C.ce[at]);
-    const float aa[4] = {a4.x, a4.y, a4.z, a4.w};
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float4 &s = S[4 * p + r];
-      s = make_float4(s.x * aa[r], s.y * aa[r], s.z * aa[r], s.w * aa[r]);
-    }
+    for (int r = 0; r < 4; r += 2) {
+      ulonglong2 a = make_ulonglong2(cl, cl);
+      // with the channel gate a lone token's decay stands where the two's does
+      if (KDA) a = *reinterpret_cast<const ulonglong2 *>(&C.cu[f / 2][at + r]);
 #pragma unroll
-    for (int m = 0; m < B; ++m) {
-      const float4 k4 = lds4(KDA ? &C.ke[m][at] : &R.k[m][at]);
-      const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
+      for (int i = 0; i < 2; ++i) {
+        S[4 * p + r][i] = mul2(S[4 * p + r][i], a.x);
+        S[4 * p + r + 1][i] = mul2(S[4 * p + r + 1][i], a.y);
+      }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float4 &s = S[4 * p + r];
-        s.x += w[m].x * kk[r]; s.y += w[m].y * kk[r]; s.z += w[m].z * kk[r]; s.w += w[m].w * kk[r];
+      for (int m = 0; m < B; ++m) {
+        const ulonglong2 k =
+            *reinterpret_cast<const ulonglong2 *>((KDA ? C.ku[f + m] : C.kx[f + m]) + at + r);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          S[4 * p + r][i] = fma2(w[m][i], k.x, S[4 * p + r][i]);
+          S[4 * p + r + 1][i] = fma2(w[m][i], k.y, S[4 * p + r + 1][i]);
+        }
       }
     }
   }
 }
 
-// FULL: d_k = 32 NP and d_v = 128, so that no row or column needs a check.
+// Four columns of a state row, as two pairs.
+__device__ __forceinline__ void load_pairs(const float *p, Pair (&s)[2]) {
+  const float4 v = ld4_stream(p);
+  s[0] = pair(v.x, v.y);
+  s[1] = pair(v.z, v.w);
+}
+__device__ __forceinline__ void load_pairs(const __nv_bfloat16 *p, Pair (&s)[2]) {
+  const float4 v = ld4_stream(p);
+  s[0] = pair(v.x, v.y);
+  s[1] = pair(v.z, v.w);
+}
+template <typename ST>
+__device__ __forceinline__ void store_pairs(ST *p, const Pair (&s)[2]) {
+  const float2 a = unpair(s[0]), b = unpair(s[1]);
+  st4_stream(p, make_float4(a.x, a.y, b.x, b.y));
+}
+
+// FULL: d_k = d_v = 128 (NP = 4), so that no row or column needs a check.
 template <typename T, typename ST, bool KDA, int NP, bool FULL>
 __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const __grid_constant__ RecArgs A) {
   __shared__ RecShared<KDA> sm;
@@ -347,26 +363,28 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
   const int col = col0 + wcol + 4 * cg;
   const bool col_ok = FULL || col < dv;
   ST *st = static_cast<ST *>(A.pool) + (int64_t(bad ? 0 : slot) * A.Hv + h) * dk * dv + col + 4 * rg * dv;
-  float4 S[NP * 4];
-#pragma unroll
-  for (int i = 0; i < NP * 4; ++i) {
-    const int j = 32 * (i >> 2) + (i & 3);            // row less 4 rg
-    S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!bad && !fresh && (FULL || (col_ok && j + 4 * rg < dk))) S[i] = ld4_stream(st + j * dv);
-  }
-
-  // Blocks of up to four tokens; none crosses the point after which the state is kept.
-  auto block_len = [&](int p) { return min(kBlock, (p < keep ? keep : len) - p); };
-  int p0 = 0, n0 = bad ? 0 : block_len(0), p1 = p0 + n0, n1 = bad ? 0 : block_len(p1);
+  Pair S[NP * 4][2];
+  // d_v known: the rows lie at constant offsets. Otherwise the pointer steps
+  // from row to row, kept from the compiler, which would hold them all.
   {
-    RecToken<KDA> r;
-    fetch<T, KDA>(A, t0 + int64_t(p0) + warp, warp < n0, h, hk, col0, lane, r);
-    put<KDA>(sm.rows[0], warp, warp < n0, lane, dk, r);
-    if (n1 > 0) {
-      fetch<T, KDA>(A, t0 + int64_t(p1) + warp, warp < n1, h, hk, col0, lane, r);
-      put<KDA>(sm.rows[1], warp, warp < n1, lane, dk, r);
+    const ST *src = st;
+#pragma unroll
+    for (int i = 0; i < NP * 4; ++i) {
+      const int j = 32 * (i >> 2) + (i & 3);            // row less 4 rg
+      S[i][0] = S[i][1] = pair(0.f, 0.f);
+      if (!bad && !fresh && (FULL || (col_ok && j + 4 * rg < dk))) load_pairs(FULL ? st + j * dv : src, S[i]);
+      if (!FULL) {
+        src += ((i & 3) == 3 ? 29 : 1) * dv;
+        asm volatile("" : "+l"(src));
+      }
     }
   }
+
+  // Groups of up to four tokens; none crosses the point after which the state is kept.
+  auto group_len = [&](int p) { return min(kGroup, (p < keep ? keep : len) - p); };
+  int p0 = 0, n0 = bad ? 0 : group_len(0), p1 = p0 + n0, n1 = bad ? 0 : group_len(p1);
+  if (warp < n0) fetch<T, KDA>(A, t0 + int64_t(p0) + warp, h, hk, col0, lane, sm.rows[0], sm.v[0], warp);
+  if (warp < n1) fetch<T, KDA>(A, t0 + int64_t(p1) + warp, h, hk, col0, lane, sm.rows[1], sm.v[1], warp);
   if (A.slots && !bad)
     for (int m = tid; m < A.N; m += kRecWarps * 32)
       if (A.slots[m] == slot && m != n) {
@@ -374,6 +392,8 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
         const int km = A.keep ? A.keep[m] : lm;
         if (lm > 0 && (keep > 0 || km > 0)) bad = true;
       }
+  land<T, KDA>(A, warp < n0, col0, lane, sm.rows[0], sm.v[0], warp);
+  if (n1 > 0) land<T, KDA>(A, warp < n1, col0, lane, sm.rows[1], sm.v[1], warp);
   bad = __syncthreads_or(bad);
 
   const int64_t o_stride = int64_t(A.Hv) * dv;
@@ -388,30 +408,39 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
   relate<KDA>(sm.rows[0], sm.coef[0], warp, n0, lane);
   __syncthreads();
 
+  const bool idle = !FULL && col0 + wcol >= dv;         // warps behind the last column
   for (int b = 0, slot3 = 0;; ++b) {
-    const int p2 = p1 + n1, n2 = block_len(p2);      // 0 at the run's end
-    RecToken<KDA> r;
-    if (n2 > 0) fetch<T, KDA>(A, t0 + int64_t(p2) + warp, warp < n2, h, hk, col0, lane, r);
+    const int p2 = p1 + n1, n2 = group_len(p2);      // 0 at the run's end
     const int slot1 = slot3 == 2 ? 0 : slot3 + 1, slot2 = slot3 == 0 ? 2 : slot3 - 1;
-    if (n1 > 0) relate<KDA>(sm.rows[slot1], sm.coef[(b + 1) & 1], warp, n1, lane);
-    const RecRows<KDA> &R = sm.rows[slot3];
+    if (warp < n2)
+      fetch<T, KDA>(A, t0 + int64_t(p2) + warp, h, hk, col0, lane, sm.rows[b & 1], sm.v[slot2], warp);
+    if (n1 > 0) relate<KDA>(sm.rows[(b + 1) & 1], sm.coef[(b + 1) & 1], warp, n1, lane);
     const RecCoef<KDA> &C = sm.coef[b & 1];
-    T *ob = o + p0 * o_stride;
-    if (n0 > 2)
-      block_step<T, KDA, NP, 4>(R, C, sm.u[warp], S, n0, lane, wcol, ob, o_stride, col_ok);
-    else if (n0 == 2)
-      block_step<T, KDA, NP, 2>(R, C, sm.u[warp], S, n0, lane, wcol, ob, o_stride, col_ok);
-    else
-      block_step<T, KDA, NP, 1>(R, C, sm.u[warp], S, n0, lane, wcol, ob, o_stride, col_ok);
-    if (p1 == keep) {
+    if (!idle) {
+      const bool more = n1 > 0 || p1 == keep;        // the state after this group is wanted
+      T *ob = o + p0 * o_stride;
+      for (int f = 0; f < n0; f += 2) {
+        const bool update = more || f + 2 < n0;
+        if (f + 1 < n0)
+          step<T, KDA, NP, 2>(sm.v[slot3], C, f, sm.u[warp], S, lane, wcol, ob + f * o_stride, o_stride, col_ok, update);
+        else
+          step<T, KDA, NP, 1>(sm.v[slot3], C, f, sm.u[warp], S, lane, wcol, ob + f * o_stride, o_stride, col_ok, update);
+      }
+      if (p1 == keep) {
+        ST *dst = st;
 #pragma unroll
-      for (int i = 0; i < NP * 4; ++i) {
-        const int j = 32 * (i >> 2) + (i & 3);
-        if (FULL || (col_ok && j + 4 * rg < dk)) st4_stream(st + j * dv, S[i]);
+        for (int i = 0; i < NP * 4; ++i) {
+          const int j = 32 * (i >> 2) + (i & 3);
+          if (FULL || (col_ok && j + 4 * rg < dk)) store_pairs(FULL ? st + j * dv : dst, S[i]);
+          if (!FULL) {
+            dst += ((i & 3) == 3 ? 29 : 1) * dv;
+            asm volatile("" : "+l"(dst));
+          }
+        }
       }
     }
     if (n1 == 0) break;
-    if (n2 > 0) put<KDA>(sm.rows[slot2], warp, warp < n2, lane, dk, r);
+    if (n2 > 0) land<T, KDA>(A, warp < n2, col0, lane, sm.rows[b & 1], sm.v[slot2], warp);
     __syncthreads();
     p0 = p1; n0 = n1; p1 = p2; n1 = n2;
     slot3 = slot1;
@@ -613,6 +642,17 @@ __global__ void __launch_bounds__(32 * kOneWarps<ST, FULL>, 16 / kOneWarps<ST, F
 
 template <typename T, typename ST, bool KDA, int NP>
 cudaError_t launch_np(RecArgs &A, cudaStream_t s) {
+  A.splits = (A.dv + kRecCols - 1) / kRecCols;
+  const unsigned grid = unsigned(A.N) * A.Hv * A.splits;
+  if (NP == 4 && A.dk == 128 && A.dv == 128)
+    gdn_recurrent_kernel<T, ST, KDA, 4, true><<<grid, kRecWarps * 32, 0, s>>>(A);
+  else
+    gdn_recurrent_kernel<T, ST, KDA, NP, false><<<grid, kRecWarps * 32, 0, s>>>(A);
+  return cudaGetLastError();
+}
+
+template <typename T, typename ST, bool KDA>
+cudaError_t launch_gate(RecArgs &A, cudaStream_t s) {
   // One token a run goes to its own kernel, where the rows come in whole pieces.
   if (!A.cu && A.L == 1 && A.dv % Piece<ST>::n == 0) {
     const unsigned units = unsigned(A.N) * A.Hv;
@@ -622,20 +662,13 @@ cudaError_t launch_np(RecArgs &A, cudaStream_t s) {
       gdn_recurrent_one_kernel<T, ST, KDA, false><<<units, 32 * kOneWarps<ST, false>, 0, s>>>(A);
     return cudaGetLastError();
   }
-  A.splits = (A.dv + kRecCols - 1) / kRecCols;
-  const unsigned grid = unsigned(A.N) * A.Hv * A.splits;
-  if (A.dk == 32 * NP && A.dv == 128)
-    gdn_recurrent_kernel<T, ST, KDA, NP, true><<<grid, kRecWarps * 32, 0, s>>>(A);
-  else
-    gdn_recurrent_kernel<T, ST, KDA, NP, false><<<grid, kRecWarps * 32, 0, s>>>(A);
-  return cudaGetLastError();
+  if (A.dk <= 64) return launch_np<T, ST, KDA, 2>(A, s);
+  return A.dk <= 96 ? launch_np<T, ST, KDA, 3>(A, s) : launch_np<T, ST, KDA, 4>(A, s);
 }
 
 template <typename T, typename ST>
 cudaError_t launch_types(RecArgs &A, bool kda, cudaStream_t s) {
-  if (A.dk <= 64)
-    return kda ? launch_np<T, ST, true, 2>(A, s) : launch_np<T, ST, false, 2>(A, s);
-  return kda ? launch_np<T, ST, true, 4>(A, s) : launch_np<T, ST, false, 4>(A, s);
+  return kda ? launch_gate<T, ST, true>(A, s) : launch_gate<T, ST, false>(A, s);
 }
 
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -681,7 +714,7 @@ extern "C" int gdn_recurrent_fwd(const void *q, const void *k, const void *v, co
   A.N = N; A.T = T; A.L = cu_seqlens ? 0 : T / N;
   A.Hk = H_k; A.Hv = H_v; A.dk = d_k; A.dv = d_v;
   A.vec = d_k % 4 == 0 && q_stride % 4 == 0 && k_stride % 4 == 0 && v_stride % 4 == 0 &&
-          aligned(q, 4 * e) && aligned(k, 4 * e) && aligned(v, 4 * e);
+          aligned(q, 4 * e) && aligned(k, 4 * e) && aligned(v, 4 * e) && (!channel_gate || aligned(g, 16));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t err;
   if (dtype == GDN_BF16)
