@@ -7,34 +7,33 @@
 //   x_i = sum_j st[j][i] a_j k_j,  u_i = beta (v_i - x_i)
 //   st[j][i] <- a_j st[j][i] + u_i k_j,  o_i = sum_j st[j][i] q_j
 //
-// Two tokens are taken together, so that a pass over the state serves both and
-// the chain from token to token runs over a few scalars. With S the state
-// before the two, c_m = a_0 .. a_m:
+// Up to four tokens are taken together, so that a pass over the state serves
+// all of them and the chain from token to token runs over a few scalars. With
+// S the state before the group, c_m = a_0 .. a_m, d_ml = a_(l+1) .. a_m:
 //   X_m = S^T k_m,  Y_m = S^T q_m                    (one pass, one reduction)
-//   u_0 = beta_0 (v_0 - c_0 X_0),  u_1 = beta_1 (v_1 - c_1 X_1 - a_1 (k_0 . k_1) u_0)
-//   o_0 = c_0 Y_0 + (k_0 . q_0) u_0,  o_1 = c_1 Y_1 + a_1 (k_0 . q_1) u_0 + (k_1 . q_1) u_1
-//   S  <- c_1 S + a_1 u_0 k_0 + u_1 k_1              (one pass)
+//   u_m = beta_m (v_m - c_m X_m - sum_(l<m) d_ml (k_l . k_m) u_l)
+//   o_m = c_m Y_m + sum_(l<=m) d_ml (k_l . q_m) u_l
+//   S  <- c_last S + sum_l d_(last,l) u_l k_l         (one pass)
 // With the channel gate the products of decays sit inside the dot products and
 // in rows of k and q scaled by them. All of them are products of the tokens'
 // own decays, never quotients, so a decay of zero is as good as any other.
 //
-// A warp owns 16 columns i and all rows j of one state; columns of st evolve
-// independently, so warps exchange nothing of the state. Lane (rg, cg) =
-// (lane / 4, lane % 4) holds columns 4 cg .. 4 cg + 3 of rows 32 p + 4 rg + r
-// (r < 4, p < d_k / 32) in registers for the whole run: HBM sees one read and
-// one write of the state however many tokens the run has. The partial sums are
-// reduced over the eight rg lanes by halving (7 shuffles a token), after which
-// one lane holds a column's X of every token and its neighbour the Y.
+// A CTA of four warps owns 64 columns i and all rows j of one state, in
+// registers for the whole run: HBM sees one read and one write of the state
+// however many tokens the run has. Lane (sub, cl) = (lane / 16, lane % 16) of a
+// warp holds columns 4 cl .. 4 cl + 3 of rows 32 p + 4 g + r (g = 2 warp + sub,
+// r < 4, p < d_k / 32). The two sub lanes add up their X and Y by a shuffle,
+// the four warps through shared memory; then one thread has a column's X of
+// every token and another its Y, which makes the chain over a group's tokens
+// two barriers long. (With all rows of 16 columns in one warp and three
+// shuffles instead, two tokens a pass, 64 tokens of one state took 39 us.)
 //
-// (Four together take no fewer multiply-adds a token and half as many steps,
-// but 64 more registers and twice the code: 63 us against 47 us for 64 runs of
-// one to six tokens of 32 heads.)
-//
-// k, q, v and the decays of up to four tokens at a time come through shared
-// memory in fp32, a token a warp: the rows of the group after next are on their
-// way from HBM, those of the next are multiplied with each other, while this
-// one is computed. k and q lie there twice over, k_j k_j, so that one 16-byte
-// read gives the operands of paired multiply-adds for two rows.
+// k, q, v and the decays of a group come through shared memory in fp32, a token
+// a warp: the rows of the group after next are on their way from HBM, those of
+// the next are multiplied with each other, while this one is computed. k and q
+// lie there twice over, k_j k_j, so that one 16-byte read gives the operands of
+// paired multiply-adds for two rows (2.2 cycles for 64 products a scheduler,
+// against 2.9 for two single ones).
 #include "gdn_internal.cuh"
 #include "rows.cuh"
 
@@ -42,7 +41,7 @@ namespace gdn {
 namespace {
 
 constexpr int kRecWarps = 4, kRecCols = 16 * kRecWarps;   // columns of d_v per CTA
-constexpr int kGroup = 4;                                 // tokens staged together
+constexpr int kGroup = 4;                                 // tokens taken together
 
 struct RecArgs {
   const void *q, *k, *v;
@@ -66,26 +65,28 @@ struct alignas(16) RecRows {
   float a[kGroup][KDA ? 128 : 4];
   float beta[kGroup];
 };
-// What the passes over the state take: rows twice over, and for each pair of
-// tokens m = 0, 1 the scalars.
+// What follows from them: rows of k and q twice over (channel gate: c_m k_m, c_m
+// q_m), and the scalars of the chain.
 template <bool KDA>
 struct alignas(16) RecCoef {
-  float2 kx[kGroup][128], qx[kGroup][128];   // k and q (channel gate: c_m k_m, c_m q_m)
-  float2 ku[KDA ? kGroup : 1][128];          // channel gate: the second of the two's decay times k_m
-  float2 cu[KDA ? kGroup / 2 : 1][128];      // channel gate: c of the two, per row
-  float4 s[kGroup];                          // c_m, beta_m, then d k_0 . k_1 and k_m . q_m
-  float dq[kGroup], e[kGroup];               // d k_0 . q_1 (second tokens); decay after m in the two
+  float2 kx[kGroup][128], qx[kGroup][128];
+  float ku[KDA ? kGroup : 1][128];              // channel gate: d_(last, m) k_m
+  float cu[KDA ? 128 : 4];                      // channel gate: c_last
+  float A[kGroup][kGroup], P[kGroup][kGroup];   // [m][l]: d_ml (k_l . k_m), d_ml (k_l . q_m)
+  float c[kGroup], e[kGroup], beta[kGroup];     // c_m and d_(last, m); 1 with the channel gate
 };
 template <bool KDA>
 struct alignas(16) RecShared {
   RecRows<KDA> rows[2];              // of the next group; being fetched for the one after
   RecCoef<KDA> coef[2];              // of this group and of the next
   float v[3][kGroup][kRecCols];      // of all three
-  float u[kRecWarps][2][16];
+  float part[kRecWarps][2 * kGroup][kRecCols];   // the warps' X_0 .. X_3, Y_0 .. Y_3
+  float u[kGroup][kRecCols], ue[kGroup][kRecCols];   // u_m; d_(last, m) u_m
 };
 static_assert(sizeof(RecRows<false>) % 16 == 0 && sizeof(RecRows<true>) % 16 == 0 &&
               sizeof(RecCoef<false>) % 16 == 0 && sizeof(RecCoef<true>) % 16 == 0 &&
-              offsetof(RecCoef<false>, s) % 16 == 0 && offsetof(RecRows<false>, a) % 16 == 0,
+              offsetof(RecCoef<false>, ku) % 16 == 0 && offsetof(RecCoef<true>, cu) % 16 == 0 &&
+              offsetof(RecRows<false>, a) % 16 == 0,
               "rows are read in 16-byte pieces");
 
 template <typename T>
@@ -187,134 +188,64 @@ __device__ __forceinline__ void put_twice(float2 *p, float4 x) {
   *reinterpret_cast<float4 *>(p + 2) = make_float4(x.z, x.z, x.w, x.w);
 }
 
-// Warp m works out what token m has to do with the one before it. nb: tokens of
+// One warp works out what token m has to do with those before it. nb: tokens of
 // the group.
 template <bool KDA>
 __device__ __forceinline__ void relate(const RecRows<KDA> &R, RecCoef<KDA> &C, int m, int nb, int lane) {
-  const int c = lane * 4, f = m & ~1;                 // f: the first of the two
-  if (f >= nb) return;
-  const bool second = m & 1;
-  const float4 km = lds4(&R.k[m][c]), qm = lds4(&R.q[m][c]), kf = lds4(&R.k[f][c]);
-  float4 kd = km, qd = qm;                            // with the decay since the first
-  float am = 1.f, a0 = 1.f, a1 = 1.f;
-  if (KDA) {
-    const float4 a = lds4(&R.a[m][c]);
-    float4 x = a;                                     // c_m
-    if (second) {
-      kd = mul4(km, a);
-      qd = mul4(qm, a);
-      x = mul4(a, lds4(&R.a[f][c]));
+  if (m >= nb) return;
+  const int c = lane * 4;
+  const float4 km = lds4(&R.k[m][c]), qm = lds4(&R.q[m][c]);
+  float z[8];                         // k_l . k_m (l = 0..3), k_l . q_m
+  float4 kd = km, qd = qm;            // with the decays since l
+#pragma unroll
+  for (int l = kGroup - 1; l >= 0; --l) {
+    z[l] = z[4 + l] = 0.f;
+    if (l > m) continue;
+    const float4 kl = lds4(&R.k[l][c]);
+    if (KDA && l < m) {
+      const float4 a = lds4(&R.a[l + 1][c]);
+      kd = mul4(kd, a);
+      qd = mul4(qd, a);
     }
-    put_twice(&C.kx[m][c], mul4(km, x));
-    put_twice(&C.qx[m][c], mul4(qm, x));
-    put_twice(&C.ku[m][c], second ? km : mul4(km, lds4(&R.a[f + 1][c])));
-    if (second) put_twice(&C.cu[f / 2][c], x);
+    z[l] = dot4(kl, kd);
+    z[4 + l] = dot4(kl, qd);
+  }
+  if (KDA) {
+    const float4 a0 = lds4(&R.a[0][c]);
+    put_twice(&C.kx[m][c], mul4(kd, a0));
+    put_twice(&C.qx[m][c], mul4(qd, a0));
+    float4 e = make_float4(1.f, 1.f, 1.f, 1.f);
+    for (int l = m + 1; l < nb; ++l) e = mul4(e, lds4(&R.a[l][c]));
+    sts4(&C.ku[m][c], mul4(km, e));
+    if (m == 0) sts4(&C.cu[c], mul4(a0, e));
   } else {
     put_twice(&C.kx[m][c], km);
     put_twice(&C.qx[m][c], qm);
-    a0 = R.a[f][0];
-    a1 = R.a[f + 1][0];
-    am = a1;
   }
-  const float kk = warp_sum(second ? dot4(kf, kd) : 0.f), kq = warp_sum(dot4(km, qm));
-  const float dq = warp_sum(second ? dot4(kf, qd) : 0.f);
-  if (lane == 0) {
-    C.s[m] = make_float4(KDA ? 1.f : second ? a0 * a1 : a0, R.beta[m], am * kk, kq);
-    C.dq[m] = am * dq;
-    C.e[m] = second ? 1.f : a1;
-  }
-}
-
-// The tokens f, f + 1 of a group (B = 1: f alone) on a warp's columns; update:
-// whether the state after them is wanted.
-template <typename T, bool KDA, int NP, int B>
-__device__ __forceinline__ void step(const float (*v)[kRecCols], const RecCoef<KDA> &C, int f, float (*us)[16],
-                                     Pair (&S)[NP * 4][2], int lane, int wcol, T *o, int64_t o_stride,
-                                     bool col_ok, bool update) {
-  const int rg = lane >> 2, cg = lane & 3;
-  Pair xy[2 * B][2];                  // X_0.., Y_0.. of two pairs of columns, this lane's rows
+  // sum over the warp by halving: lane bits 4, 3, 2 pick one of the eight
+  float y4[4], y2[2], y;
 #pragma unroll
-  for (int m = 0; m < 2 * B; ++m) xy[m][0] = xy[m][1] = pair(0.f, 0.f);
+  for (int i = 0; i < 4; ++i)
+    y4[i] = (lane & 16 ? z[4 + i] : z[i]) + __shfl_xor_sync(~0u, lane & 16 ? z[i] : z[4 + i], 16);
 #pragma unroll
-  for (int p = 0; p < NP; ++p) {
+  for (int i = 0; i < 2; ++i)
+    y2[i] = (lane & 8 ? y4[2 + i] : y4[i]) + __shfl_xor_sync(~0u, lane & 8 ? y4[i] : y4[2 + i], 8);
+  y = (lane & 4 ? y2[1] : y2[0]) + __shfl_xor_sync(~0u, lane & 4 ? y2[0] : y2[1], 4);
+  y += __shfl_xor_sync(~0u, y, 2);
+  y += __shfl_xor_sync(~0u, y, 1);
+  const int l = (lane >> 2) & 3;
+  float d = 1.f, cm = 1.f, e = 1.f;
+  if (!KDA) {
 #pragma unroll
-    for (int m = 0; m < 2 * B; ++m) {
-      const float2 *row = (m < B ? C.kx[f + m] : C.qx[f + m - B]) + 32 * p + 4 * rg;
-#pragma unroll
-      for (int r = 0; r < 4; r += 2) {
-        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(row + r);
-        xy[m][0] = fma2(S[4 * p + r][0], w.x, xy[m][0]);
-        xy[m][1] = fma2(S[4 * p + r][1], w.x, xy[m][1]);
-        xy[m][0] = fma2(S[4 * p + r + 1][0], w.y, xy[m][0]);
-        xy[m][1] = fma2(S[4 * p + r + 1][1], w.y, xy[m][1]);
-      }
+    for (int i = 0; i < kGroup; ++i) {
+      const float a = R.a[i][0];
+      if (i <= m) cm *= a;
+      if (i <= m && i > l) d *= a;
+      if (i > m && i < nb) e *= a;
     }
   }
-  // Halving: lane bit 4 picks columns 2, 3; bit 3 the odd one; bit 2 Y.
-  const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
-  float t1[2 * B], z[B];
-#pragma unroll
-  for (int m = 0; m < 2 * B; ++m) {
-    const float2 lo2 = unpair(b4 ? xy[m][1] : xy[m][0]), give = unpair(b4 ? xy[m][0] : xy[m][1]);
-    const float lo = lo2.x + __shfl_xor_sync(~0u, give.x, 16);
-    const float hi = lo2.y + __shfl_xor_sync(~0u, give.y, 16);
-    t1[m] = (b3 ? hi : lo) + __shfl_xor_sync(~0u, b3 ? lo : hi, 8);
-  }
-#pragma unroll
-  for (int m = 0; m < B; ++m)
-    z[m] = (b2 ? t1[B + m] : t1[m]) + __shfl_xor_sync(~0u, b2 ? t1[m] : t1[B + m], 4);
-  const int c = cg * 4 + (b4 ? 2 : 0) + (b3 ? 1 : 0);     // this lane's column of the warp's 16
-  // u in the X lanes; the Y lanes take it from there
-  const float4 s0 = C.s[f], s1 = C.s[f + B - 1];
-  const float z0 = KDA ? z[0] : s0.x * z[0], z1 = KDA ? z[B - 1] : s1.x * z[B - 1];
-  const float u0x = s0.y * (v[f][wcol + c] - z0);
-  const float u1x = B == 2 ? s1.y * (v[f + 1][wcol + c] - z1 - s1.z * u0x) : 0.f;
-  const float u0o = __shfl_xor_sync(~0u, u0x, 4), u1o = B == 2 ? __shfl_xor_sync(~0u, u1x, 4) : 0.f;
-  if (b2) {
-    if (col_ok) {
-      o[c] = from_f32<T>(z0 + s0.w * u0o);
-      if (B == 2) o[o_stride + c] = from_f32<T>(z1 + C.dq[f + 1] * u0o + s1.w * u1o);
-    }
-  } else {
-    us[0][c] = B == 2 && !KDA ? C.e[f] * u0x : u0x;
-    if (B == 2) us[1][c] = u1x;
-  }
-  __syncwarp();
-  if (!update) return;
-  Pair w[B][2];
-#pragma unroll
-  for (int m = 0; m < B; ++m) {
-    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&us[m][4 * cg]);
-    w[m][0] = x.x;
-    w[m][1] = x.y;
-  }
-  __syncwarp();                       // read before the next pair's are written
-  const Pair cl = pair(s1.x, s1.x);
-#pragma unroll
-  for (int p = 0; p < NP; ++p) {
-    const int at = 32 * p + 4 * rg;
-#pragma unroll
-    for (int r = 0; r < 4; r += 2) {
-      ulonglong2 a = make_ulonglong2(cl, cl);
-      // with the channel gate a lone token's decay stands where the two's does
-      if (KDA) a = *reinterpret_cast<const ulonglong2 *>(&C.cu[f / 2][at + r]);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        S[4 * p + r][i] = mul2(S[4 * p + r][i], a.x);
-        S[4 * p + r + 1][i] = mul2(S[4 * p + r + 1][i], a.y);
-      }
-#pragma unroll
-      for (int m = 0; m < B; ++m) {
-        const ulonglong2 k =
-            *reinterpret_cast<const ulonglong2 *>((KDA ? C.ku[f + m] : C.kx[f + m]) + at + r);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          S[4 * p + r][i] = fma2(w[m][i], k.x, S[4 * p + r][i]);
-          S[4 * p + r + 1][i] = fma2(w[m][i], k.y, S[4 * p + r + 1][i]);
-        }
-      }
-    }
-  }
+  if ((lane & 3) == 0) (lane & 16 ? C.P : C.A)[m][l] = d * y;
+  if (lane == 0) { C.c[m] = cm; C.e[m] = e; C.beta[m] = R.beta[m]; }
 }
 
 // Four columns of a state row, as two pairs.
@@ -359,10 +290,10 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
   const int keep = A.keep ? kept : len;
   bool bad = slot >= A.num_slots || keep < 0 || keep > len;
 
-  const int col0 = split * kRecCols, wcol = warp * 16, rg = lane >> 2, cg = lane & 3;
-  const int col = col0 + wcol + 4 * cg;
+  const int col0 = split * kRecCols, cl = 4 * (lane & 15), g4 = 4 * (2 * warp + (lane >> 4));
+  const int col = col0 + cl;
   const bool col_ok = FULL || col < dv;
-  ST *st = static_cast<ST *>(A.pool) + (int64_t(bad ? 0 : slot) * A.Hv + h) * dk * dv + col + 4 * rg * dv;
+  ST *st = static_cast<ST *>(A.pool) + (int64_t(bad ? 0 : slot) * A.Hv + h) * dk * dv + col + g4 * dv;
   Pair S[NP * 4][2];
   // d_v known: the rows lie at constant offsets. Otherwise the pointer steps
   // from row to row, kept from the compiler, which would hold them all.
@@ -370,9 +301,9 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
     const ST *src = st;
 #pragma unroll
     for (int i = 0; i < NP * 4; ++i) {
-      const int j = 32 * (i >> 2) + (i & 3);            // row less 4 rg
+      const int j = 32 * (i >> 2) + (i & 3);            // row less g4
       S[i][0] = S[i][1] = pair(0.f, 0.f);
-      if (!bad && !fresh && (FULL || (col_ok && j + 4 * rg < dk))) load_pairs(FULL ? st + j * dv : src, S[i]);
+      if (!bad && !fresh && (FULL || (col_ok && j + g4 < dk))) load_pairs(FULL ? st + j * dv : src, S[i]);
       if (!FULL) {
         src += ((i & 3) == 3 ? 29 : 1) * dv;
         asm volatile("" : "+l"(src));
@@ -397,51 +328,142 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
   bad = __syncthreads_or(bad);
 
   const int64_t o_stride = int64_t(A.Hv) * dv;
-  T *o = static_cast<T *>(A.o) + (int64_t(t0) * A.Hv + h) * dv + col0 + wcol;
+  T *o = static_cast<T *>(A.o) + (int64_t(t0) * A.Hv + h) * dv + col0;
   if (bad) {   // outputs that cannot be mistaken for results; the state is left alone
     if (tid == 0 && A.status) atomicOr(A.status, kErrBadSeqlens);
     const float nan = __int_as_float(0x7fffffff);
-    if (col_ok && rg == 0)
-      for (int t = 0; t < len; ++t) st4(o + t * o_stride + 4 * cg, make_float4(nan, nan, nan, nan));
+    if (col_ok && g4 == 0)
+      for (int t = 0; t < len; ++t) st4(o + t * o_stride + cl, make_float4(nan, nan, nan, nan));
     return;
   }
   relate<KDA>(sm.rows[0], sm.coef[0], warp, n0, lane);
   __syncthreads();
 
-  const bool idle = !FULL && col0 + wcol >= dv;         // warps behind the last column
+  const bool ylane = warp >= kRecWarps / 2;             // this thread's part of the chain: Y or X
+  const int c = tid % kRecCols;                         // of this column
+  const bool c_ok = FULL || col0 + c < dv;
   for (int b = 0, slot3 = 0;; ++b) {
     const int p2 = p1 + n1, n2 = group_len(p2);      // 0 at the run's end
     const int slot1 = slot3 == 2 ? 0 : slot3 + 1, slot2 = slot3 == 0 ? 2 : slot3 - 1;
     if (warp < n2)
       fetch<T, KDA>(A, t0 + int64_t(p2) + warp, h, hk, col0, lane, sm.rows[b & 1], sm.v[slot2], warp);
-    if (n1 > 0) relate<KDA>(sm.rows[(b + 1) & 1], sm.coef[(b + 1) & 1], warp, n1, lane);
     const RecCoef<KDA> &C = sm.coef[b & 1];
-    if (!idle) {
-      const bool more = n1 > 0 || p1 == keep;        // the state after this group is wanted
-      T *ob = o + p0 * o_stride;
-      for (int f = 0; f < n0; f += 2) {
-        const bool update = more || f + 2 < n0;
-        if (f + 1 < n0)
-          step<T, KDA, NP, 2>(sm.v[slot3], C, f, sm.u[warp], S, lane, wcol, ob + f * o_stride, o_stride, col_ok, update);
-        else
-          step<T, KDA, NP, 1>(sm.v[slot3], C, f, sm.u[warp], S, lane, wcol, ob + f * o_stride, o_stride, col_ok, update);
-      }
-      if (p1 == keep) {
-        ST *dst = st;
+
+#pragma unroll 1
+    for (int m = 0; m < n0; ++m) {
+      Pair x[2] = {pair(0.f, 0.f), pair(0.f, 0.f)}, y[2] = {x[0], x[0]};
 #pragma unroll
-        for (int i = 0; i < NP * 4; ++i) {
-          const int j = 32 * (i >> 2) + (i & 3);
-          if (FULL || (col_ok && j + 4 * rg < dk)) store_pairs(FULL ? st + j * dv : dst, S[i]);
-          if (!FULL) {
-            dst += ((i & 3) == 3 ? 29 : 1) * dv;
-            asm volatile("" : "+l"(dst));
+      for (int i = 0; i < NP * 4; i += 2) {
+        const int j = 32 * (i >> 2) + (i & 3) + g4;
+        const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(&C.kx[m][j]);
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(&C.qx[m][j]);
+        x[0] = fma2(S[i][0], k.x, x[0]);
+        x[1] = fma2(S[i][1], k.x, x[1]);
+        y[0] = fma2(S[i][0], q.x, y[0]);
+        y[1] = fma2(S[i][1], q.x, y[1]);
+        x[0] = fma2(S[i + 1][0], k.y, x[0]);
+        x[1] = fma2(S[i + 1][1], k.y, x[1]);
+        y[0] = fma2(S[i + 1][0], q.y, y[0]);
+        y[1] = fma2(S[i + 1][1], q.y, y[1]);
+      }
+      // the lower sixteen lanes take columns 0 and 1 of four, the upper ones 2 and 3
+      const bool up = lane & 16;
+      const float2 xk = unpair(up ? x[1] : x[0]), xg = unpair(up ? x[0] : x[1]);
+      const float2 yk = unpair(up ? y[1] : y[0]), yg = unpair(up ? y[0] : y[1]);
+      float2 xs, ys;
+      xs.x = xk.x + __shfl_xor_sync(~0u, xg.x, 16);
+      xs.y = xk.y + __shfl_xor_sync(~0u, xg.y, 16);
+      ys.x = yk.x + __shfl_xor_sync(~0u, yg.x, 16);
+      ys.y = yk.y + __shfl_xor_sync(~0u, yg.y, 16);
+      const int at = cl + (up ? 2 : 0);
+      *reinterpret_cast<float2 *>(&sm.part[warp][m][at]) = xs;
+      *reinterpret_cast<float2 *>(&sm.part[warp][kGroup + m][at]) = ys;
+    }
+    __syncthreads();
+
+    float z[kGroup];
+#pragma unroll
+    for (int m = 0; m < kGroup; ++m) {
+      z[m] = 0.f;
+      if (m < n0) {
+        const int i = (ylane ? kGroup : 0) + m;
+        z[m] = (sm.part[0][i][c] + sm.part[1][i][c]) + (sm.part[2][i][c] + sm.part[3][i][c]);
+        if (!KDA) z[m] *= C.c[m];
+      }
+    }
+    if (!ylane) {
+      float u[kGroup];
+#pragma unroll
+      for (int m = 0; m < kGroup; ++m) {
+        u[m] = 0.f;
+        if (m < n0) {
+          float x = sm.v[slot3][m][c] - z[m];
+#pragma unroll
+          for (int l = 0; l < m; ++l) x -= C.A[m][l] * u[l];
+          u[m] = C.beta[m] * x;
+          sm.u[m][c] = u[m];
+          sm.ue[m][c] = KDA ? u[m] : C.e[m] * u[m];
+        }
+      }
+    } else if (n1 > 0) {              // meanwhile: the next group's tokens, two a warp
+      relate<KDA>(sm.rows[(b + 1) & 1], sm.coef[(b + 1) & 1], 2 * (warp & 1), n1, lane);
+      relate<KDA>(sm.rows[(b + 1) & 1], sm.coef[(b + 1) & 1], 2 * (warp & 1) + 1, n1, lane);
+    }
+    __syncthreads();
+
+    if (ylane && c_ok) {
+#pragma unroll
+      for (int m = 0; m < kGroup; ++m)
+        if (m < n0) {
+          float y = z[m];
+#pragma unroll
+          for (int l = 0; l <= m; ++l) y += C.P[m][l] * sm.u[l][c];
+          o[(p0 + m) * o_stride + c] = from_f32<T>(y);
+        }
+    }
+    if (n1 > 0 || p1 == keep) {       // the state after this group is wanted
+      const Pair cl2 = KDA ? 0 : pair(C.c[n0 - 1], C.c[n0 - 1]);
+#pragma unroll
+      for (int i = 0; i < NP * 4; ++i) {
+        const float a = KDA ? C.cu[32 * (i >> 2) + (i & 3) + g4] : 0.f;
+        const Pair a2 = KDA ? pair(a, a) : cl2;
+        S[i][0] = mul2(S[i][0], a2);
+        S[i][1] = mul2(S[i][1], a2);
+      }
+#pragma unroll 1
+      for (int m = 0; m < n0; ++m) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(&sm.ue[m][cl]);
+#pragma unroll
+        for (int i = 0; i < NP * 4; i += 2) {
+          const int j = 32 * (i >> 2) + (i & 3) + g4;
+          ulonglong2 k;
+          if (KDA) {
+            const float2 f = *reinterpret_cast<const float2 *>(&C.ku[m][j]);
+            k = make_ulonglong2(pair(f.x, f.x), pair(f.y, f.y));
+          } else {
+            k = *reinterpret_cast<const ulonglong2 *>(&C.kx[m][j]);
           }
+          S[i][0] = fma2(w.x, k.x, S[i][0]);
+          S[i][1] = fma2(w.y, k.x, S[i][1]);
+          S[i + 1][0] = fma2(w.x, k.y, S[i + 1][0]);
+          S[i + 1][1] = fma2(w.y, k.y, S[i + 1][1]);
+        }
+      }
+    }
+    if (p1 == keep) {
+      ST *dst = st;
+#pragma unroll
+      for (int i = 0; i < NP * 4; ++i) {
+        const int j = 32 * (i >> 2) + (i & 3);
+        if (FULL || (col_ok && j + g4 < dk)) store_pairs(FULL ? st + j * dv : dst, S[i]);
+        if (!FULL) {
+          dst += ((i & 3) == 3 ? 29 : 1) * dv;
+          asm volatile("" : "+l"(dst));
         }
       }
     }
     if (n1 == 0) break;
     if (n2 > 0) land<T, KDA>(A, warp < n2, col0, lane, sm.rows[b & 1], sm.v[slot2], warp);
-    __syncthreads();
     p0 = p1; n0 = n1; p1 = p2; n1 = n2;
     slot3 = slot1;
   }
