@@ -53,7 +53,8 @@ struct RecArgs {
   uint32_t *status;
   int64_t q_stride, k_stride, v_stride, num_slots;
   int N, T, L, Hk, Hv, dk, dv;      // L: tokens per run without cu
-  int splits;                       // CTAs per state
+  int splits;                       // CTAs per state: 1 or 2
+  float per_k;                      // H_k / H_v
   bool vec;                         // q, k, v rows can be read four elements at a time
 };
 
@@ -88,6 +89,18 @@ static_assert(sizeof(RecRows<false>) % 16 == 0 && sizeof(RecRows<true>) % 16 == 
               offsetof(RecCoef<false>, ku) % 16 == 0 && offsetof(RecCoef<true>, cu) % 16 == 0 &&
               offsetof(RecRows<false>, a) % 16 == 0,
               "rows are read in 16-byte pieces");
+
+// Grid: x the CTAs of a run, y and z the runs.
+constexpr int kGridY = 65535;
+__device__ __forceinline__ int run_of(const RecArgs &A) { return blockIdx.y + blockIdx.z * kGridY; }
+dim3 grid_of(const RecArgs &A, int per_run) {
+  return dim3(unsigned(per_run), unsigned(A.N < kGridY ? A.N : kGridY), unsigned((A.N + kGridY - 1) / kGridY));
+}
+// h / (H_v / H_k): the middle of a head's interval, so that rounding of a few
+// 2^-24 of h < 2^20 cannot reach the next whole number.
+__device__ __forceinline__ int key_head(const RecArgs &A, int h) {
+  return int((float(h) + 0.5f) * A.per_k);
+}
 
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p, int n, bool vec) {
@@ -270,8 +283,10 @@ template <typename T, typename ST, bool KDA, int NP, bool FULL>
 __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const __grid_constant__ RecArgs A) {
   __shared__ RecShared<KDA> sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int unit = blockIdx.x / A.splits, split = blockIdx.x % A.splits;
-  const int n = unit / A.Hv, h = unit % A.Hv, hk = h / (A.Hv / A.Hk);
+  const int split = A.splits == 2 ? blockIdx.x & 1 : 0, h = A.splits == 2 ? blockIdx.x >> 1 : blockIdx.x;
+  const int n = run_of(A);
+  if (n >= A.N) return;
+  const int hk = key_head(A, h);
   const int dk = FULL ? 32 * NP : A.dk, dv = FULL ? 128 : A.dv;
 
   // The run. A bad one (tokens outside [0, T], keep outside its length, a slot
@@ -297,13 +312,16 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
   Pair S[NP * 4][2];
   // d_v known: the rows lie at constant offsets. Otherwise the pointer steps
   // from row to row, kept from the compiler, which would hold them all.
-  {
+  if (bad || fresh) {
+#pragma unroll
+    for (int i = 0; i < NP * 4; ++i) S[i][0] = S[i][1] = pair(0.f, 0.f);
+  } else {
     const ST *src = st;
 #pragma unroll
     for (int i = 0; i < NP * 4; ++i) {
       const int j = 32 * (i >> 2) + (i & 3);            // row less g4
-      S[i][0] = S[i][1] = pair(0.f, 0.f);
-      if (!bad && !fresh && (FULL || (col_ok && j + g4 < dk))) load_pairs(FULL ? st + j * dv : src, S[i]);
+      if (!FULL) S[i][0] = S[i][1] = pair(0.f, 0.f);
+      if (FULL || (col_ok && j + g4 < dk)) load_pairs(FULL ? st + j * dv : src, S[i]);
       if (!FULL) {
         src += ((i & 3) == 3 ? 29 : 1) * dv;
         asm volatile("" : "+l"(src));
@@ -530,7 +548,9 @@ __global__ void __launch_bounds__(32 * kOneWarps<ST, FULL>, 16 / kOneWarps<ST, F
   __shared__ __align__(16) float xpart[W][128], ypart[W][128];
   __shared__ float kq_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = blockIdx.x / A.Hv, h = blockIdx.x % A.Hv, hk = h / (A.Hv / A.Hk);
+  const int n = run_of(A), h = blockIdx.x;
+  if (n >= A.N) return;
+  const int hk = key_head(A, h);
   const int dk = FULL ? 128 : A.dk, dv = FULL ? 128 : A.dv;
 
   const int slot = A.slots ? A.slots[n] : n;
@@ -665,7 +685,7 @@ __global__ void __launch_bounds__(32 * kOneWarps<ST, FULL>, 16 / kOneWarps<ST, F
 template <typename T, typename ST, bool KDA, int NP>
 cudaError_t launch_np(RecArgs &A, cudaStream_t s) {
   A.splits = (A.dv + kRecCols - 1) / kRecCols;
-  const unsigned grid = unsigned(A.N) * A.Hv * A.splits;
+  const dim3 grid = grid_of(A, A.Hv * A.splits);
   if (NP == 4 && A.dk == 128 && A.dv == 128)
     gdn_recurrent_kernel<T, ST, KDA, 4, true><<<grid, kRecWarps * 32, 0, s>>>(A);
   else
@@ -677,7 +697,7 @@ template <typename T, typename ST, bool KDA>
 cudaError_t launch_gate(RecArgs &A, cudaStream_t s) {
   // One token a run goes to its own kernel, where the rows come in whole pieces.
   if (!A.cu && A.L == 1 && A.dv % Piece<ST>::n == 0) {
-    const unsigned units = unsigned(A.N) * A.Hv;
+    const dim3 units = grid_of(A, A.Hv);
     if (A.dk == 128 && A.dv == 128)
       gdn_recurrent_one_kernel<T, ST, KDA, true><<<units, 32 * kOneWarps<ST, true>, 0, s>>>(A);
     else
@@ -716,7 +736,7 @@ extern "C" int gdn_recurrent_fwd(const void *q, const void *k, const void *v, co
   if (!cu_seqlens && N > 0 && T % N) return GDN_ERR_INVALID_ARG;
   if (!slots && N > num_slots) return GDN_ERR_INVALID_ARG;
   if (d_k > 128 || d_v > 128 || d_v % 4) return GDN_ERR_UNSUPPORTED;
-  if (int64_t(N) * H_v >= (int64_t(1) << 30)) return GDN_ERR_UNSUPPORTED;
+  if (H_v >= 1 << 20 || int64_t(N) * H_v >= (int64_t(1) << 30)) return GDN_ERR_UNSUPPORTED;
   if (q_stride < int64_t(H_k) * d_k || k_stride < int64_t(H_k) * d_k ||
       v_stride < int64_t(H_v) * d_v)
     return GDN_ERR_INVALID_ARG;
@@ -734,6 +754,7 @@ extern "C" int gdn_recurrent_fwd(const void *q, const void *k, const void *v, co
   A.q_stride = q_stride; A.k_stride = k_stride; A.v_stride = v_stride;
   A.num_slots = num_slots;
   A.N = N; A.T = T; A.L = cu_seqlens ? 0 : T / N;
+  A.per_k = float(H_k) / float(H_v);
   A.Hk = H_k; A.Hv = H_v; A.dk = d_k; A.dv = d_v;
   A.vec = d_k % 4 == 0 && q_stride % 4 == 0 && k_stride % 4 == 0 && v_stride % 4 == 0 &&
           aligned(q, 4 * e) && aligned(k, 4 * e) && aligned(v, 4 * e) && (!channel_gate || aligned(g, 16));
