@@ -527,20 +527,16 @@ __device__ __forceinline__ void write_codes(const QkArgs &A, const Rows<uint8_t>
     t.a = L.na > 0 ? t.a : 0;
     t.b = L.nb > 0 ? t.b : 0;
   }
-  Row<E> z = x;
-  if (__any_sync(0xffffffffu, max(t.a, t.b) >= kInf)) {
-    // what is not finite counts for nothing, and becomes NaN
+  const bool odd = __any_sync(0xffffffffu, max(t.a, t.b) >= kInf);
+  if (odd) {                           // what is not finite counts for nothing
     uint32_t u[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      float2 f = unpair(x.v[i]);
+      const float2 f = unpair(x.v[i]);
       uint32_t &top = u[i / (E / 2)];
       const uint32_t fx = __float_as_uint(f.x) & 0x7fffffffu, fy = __float_as_uint(f.y) & 0x7fffffffu;
       if (fx < kInf) top = max(top, fx);
-      else f.x = __int_as_float(0x7fffffff);
       if (fy < kInf) top = max(top, fy);
-      else f.y = __int_as_float(0x7fffffff);
-      z.v[i] = pair(f.x, f.y);
     }
     t.a = ACC < E || L.na > 0 ? u[0] : 0;
     t.b = ACC < E || L.nb > 0 ? u[1] : 0;
@@ -586,9 +582,17 @@ __device__ __forceinline__ void write_codes(const QkArgs &A, const Rows<uint8_t>
 #pragma unroll
   for (int i = 0; i < E; i += 2) {
     const Pair inv = i < E / 2 ? pair(ia, ia) : pair(ib, ib);
-    const float2 f = unpair(mul2(z.v[i], inv)), g = unpair(mul2(z.v[i + 1], inv));
+    const float2 f = unpair(mul2(x.v[i], inv)), g = unpair(mul2(x.v[i + 1], inv));
     c[i / 2] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3) |
                uint32_t(__nv_cvt_float2_to_fp8x2(g, __NV_SATFINITE, __NV_E4M3)) << 16;
+  }
+  if (odd) {                           // infinities, 448 so far, become NaN as NaN does
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float2 f = unpair(x.v[i]);
+      if (fabsf(f.x) > 3.402823466e38f) c[i / 2] |= 0x7fu << (16 * (i & 1));
+      if (fabsf(f.y) > 3.402823466e38f) c[i / 2] |= 0x7f00u << (16 * (i & 1));
+    }
   }
   if (!on) return;
   store_codes<E, ACC>(codes.first(h), L.na, c);
