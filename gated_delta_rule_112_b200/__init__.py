@@ -475,17 +475,23 @@ class Packed(NamedTuple):
     scales: torch.Tensor
 
 
-def _rows_like(x, dtype):
+def _new_rows(x, dtype):
+    """A contiguous tensor of x's shape, and its rows."""
     if x is None:
-        return None
+        return None, None
     y = torch.empty_like(x) if x.dtype == dtype else torch.empty_like(x, dtype=dtype)
-    return y if y.is_contiguous() else torch.empty(x.shape, dtype=dtype, device="cuda")
+    if not y.is_contiguous():
+        y = torch.empty(x.shape, dtype=dtype, device="cuda")
+    _, H, d = y.shape
+    return y, _Rows(y.data_ptr(), H * d, d)
 
 
-def _packed_empty(x):
+def _new_packed(x):
+    """Packed rows for x, and their pointers."""
     T, H, d = x.shape
-    return Packed(torch.empty((T, H, d), dtype=torch.float8_e4m3fn, device="cuda"),
-                  torch.empty((T, H, (d + 31) // 32), dtype=torch.uint8, device="cuda"))
+    y = Packed(x.new_empty((T, H, d), dtype=torch.float8_e4m3fn),
+               x.new_empty((T, H, (d + 31) // 32), dtype=torch.uint8))
+    return y, _PackedRows(y.codes.data_ptr(), y.scales.data_ptr())
 
 
 def _packed_arg(name, x, dev, shape=None):
@@ -523,13 +529,16 @@ def _qk_params(name, dev, qs, ks, dtype, w_q, w_k, positions, inv_freq, norm, ep
             (positions is None) == (inv_freq is None) and (ks is not None or w_k is None)):
         raise ValueError(f"{name}: q and k [T,H,d] of bf16 or fp32, norm one of {sorted(_NORMS)}, "
                          "positions together with inv_freq, w_k only with k")
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    if not (_index(positions, torch.int32, T) and (rot == 0 or (
-            rot <= d and _index(inv_freq, torch.float64, rot // 2))) and
-            _index(w_q, dtype, d) and _index(w_k, dtype, d) and
-            _same_device(dev, positions, inv_freq, w_q, w_k)):
-        raise ValueError(f"{name}: positions int32 [T], inv_freq float64 [rot/2] with rot <= d, w_q "
-                         "and w_k [d] of the rows' dtype, contiguous, on one CUDA device")
+    rot = 0
+    if positions is not None:
+        rot = 2 * inv_freq.numel()
+        if not (_index(positions, torch.int32, T) and positions.get_device() == dev and rot <= d and
+                _index(inv_freq, torch.float64, rot // 2) and inv_freq.get_device() == dev):
+            raise ValueError(f"{name}: positions int32 [T], inv_freq float64 [rot/2] with rot <= d, "
+                             "contiguous, on the rows' device")
+    for w in (w_q, w_k):
+        if w is not None and not (_index(w, dtype, d) and w.get_device() == dev):
+            raise ValueError(f"{name}: w_q and w_k [d] of the rows' dtype, contiguous, on their device")
     return _QkParams(T, Hq, Hk, d, rot, interleaved, _NORMS[norm], _DTYPES[dtype], eps, weight_offset,
                      q_scale, rope_scale, _at(positions) if rot else None,
                      _at(inv_freq) if rot else None, _at(w_q), _at(w_k))
@@ -577,8 +586,11 @@ def qk_norm_rope_fwd(q, k, w_q=None, w_k=None, positions=None, inv_freq=None, no
     qs, ks = qx.shape, None if kx is None else kx.shape
     p = _qk_params(name, dev, qs, ks, dtype, w_q, w_k, positions, inv_freq, norm, eps, interleaved,
                    weight_offset, q_scale, rope_scale)
-    qo, ko = out if out is not None else (_rows_like(qx, dtype), _rows_like(kx, dtype))
-    qr, kr = _rows_arg(name, qo, dev, qs, dtype), _rows_arg(name, ko, dev, ks, dtype)
+    if out is None:
+        (qo, qr), (ko, kr) = _new_rows(qx, dtype), _new_rows(kx, dtype)
+    else:
+        qo, ko = out
+        qr, kr = _rows_arg(name, qo, dev, qs, dtype), _rows_arg(name, ko, dev, ks, dtype)
     s = _raw_stream(dev)
     if packed:
         rc = lib().gdn_qk_norm_rope_fwd_packed(p, _packed_arg(name, q, dev), _packed_arg(name, k, dev),
@@ -586,11 +598,11 @@ def qk_norm_rope_fwd(q, k, w_q=None, w_k=None, positions=None, inv_freq=None, no
         if rc != OK:
             _check(rc, name + "_packed")
         return qo, ko
-    q8 = _packed_empty(q) if pack else None
-    k8 = _packed_empty(k) if pack and k is not None else None
+    q8, q8p = _new_packed(q) if pack else (None, None)
+    k8, k8p = _new_packed(k) if pack and k is not None else (None, None)
     rc = lib().gdn_qk_norm_rope_fwd(p, _rows_arg(name, q, dev, qs, dtype),
                                     _rows_arg(name, k, dev, ks, dtype), qr, kr,
-                                    _packed_arg(name, q8, dev), _packed_arg(name, k8, dev), s)
+                                    q8p, k8p, s)
     if rc != OK:
         _check(rc, name)
     return (qo, ko, q8, k8) if pack else (qo, ko)
@@ -620,18 +632,20 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, w_q=None, w_k=None, positions=None, i
     if gt not in _DTYPES or (ks is None) != (dk_out is None):
         raise ValueError(f"{name}: dq_out, dk_out like the outputs, fp32 or the rows' dtype")
     dyq, dyk = _rows_arg(name, dq_out, dev, qs, gt), _rows_arg(name, dk_out, dev, ks, gt)
-    dq, dk = out if out is not None else (_rows_like(qx, dtype), _rows_like(kx, dtype))
-    d = qs[2]
-    dwq = None if w_q is None else torch.empty(d, dtype=torch.float32, device="cuda")
-    dwk = None if w_k is None else torch.empty(d, dtype=torch.float32, device="cuda")
+    if out is None:
+        (dq, qr), (dk, kr) = _new_rows(qx, dtype), _new_rows(kx, dtype)
+    else:
+        dq, dk = out
+        qr, kr = _rows_arg(name, dq, dev, qs, dtype), _rows_arg(name, dk, dev, ks, dtype)
+    dwq = None if w_q is None else torch.empty_like(w_q, dtype=torch.float32)
+    dwk = None if w_k is None else torch.empty_like(w_k, dtype=torch.float32)
     need = 0
     if dwq is not None or dwk is not None:
         need = lib().gdn_qk_norm_rope_bwd_workspace_size(p)
         if workspace is None or workspace.nbytes < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+            workspace = dq_out.new_empty(need, dtype=torch.uint8)
         elif workspace.get_device() != dev:
             raise ValueError(f"{name}: workspace on another device")
-    qr, kr = _rows_arg(name, dq, dev, qs, dtype), _rows_arg(name, dk, dev, ks, dtype)
     s = _raw_stream(dev)
     if packed:
         rc = lib().gdn_qk_norm_rope_bwd_packed(
@@ -675,13 +689,18 @@ def chunk_fwd_packed(q, k, v, g, beta, initial_state=None, cu_seqlens=None, chun
     ``chunk_fwd`` of the result, keeping q, k and v in 8 bits for
     ``chunk_bwd_packed``. q, k, v: [B,T,H,d]. Returns ``(o, final_state or None,
     Checkpoint)``; o and the state are those of the exact q, k, v."""
+    dev = q.get_device()
+    if dev < 0 or stream is not None or dev != torch.cuda.current_device():
+        with _on("chunk_fwd_packed", dev, stream):
+            return chunk_fwd_packed(q, k, v, g, beta, initial_state, cu_seqlens, chunk,
+                                    output_final_state, **norm)
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     flat = [x.reshape(B * T, H, x.shape[-1]) for x in (q, k, v)]
-    qn, kn, q8, k8 = qk_norm_rope_fwd(flat[0], flat[1], pack=True, stream=stream, **norm)
-    v8 = pack(flat[2], stream=stream)
-    o, fs = chunk_fwd(qn.view(B, T, H, dk), kn.view(B, T, H, dk), flat[2].view(B, T, H, dv).contiguous(),
-                      g, beta, initial_state, cu_seqlens, chunk, output_final_state, stream=stream)
+    qn, kn, q8, k8 = qk_norm_rope_fwd(flat[0], flat[1], pack=True, **norm)
+    v8 = pack(flat[2])
+    o, fs = chunk_fwd(qn.view(B, T, H, dk), kn.view(B, T, H, dk), flat[2].contiguous().view(B, T, H, dv),
+                      g, beta, initial_state, cu_seqlens, chunk, output_final_state)
     return o, fs, Checkpoint(q8, k8, v8, (B, T, H, dk, dv), q.dtype)
 
 
@@ -691,13 +710,18 @@ def chunk_bwd_packed(ckpt: Checkpoint, g, beta, d_o, initial_state=None, cu_seql
     that the 8-bit rows stand for. Arguments as there and for ``chunk_bwd``.
     Returns a dict: dq, dk (of the raw q, k; their dtype), dw_q, dw_k (fp32 or
     None), dv, dg, dbeta, d_initial_state (fp32)."""
+    dev = ckpt.q.codes.get_device()
+    if dev < 0 or stream is not None or dev != torch.cuda.current_device():
+        with _on("chunk_bwd_packed", dev, stream):
+            return chunk_bwd_packed(ckpt, g, beta, d_o, initial_state, cu_seqlens, d_final_state,
+                                    workspace, exact=exact, **norm)
     B, T, H, dk, dv = ckpt.shape
-    qn, kn = qk_norm_rope_fwd(ckpt.q, ckpt.k, dtype=ckpt.dtype, stream=stream, **norm)
-    v = unpack(ckpt.v, ckpt.dtype, stream=stream)
+    qn, kn = qk_norm_rope_fwd(ckpt.q, ckpt.k, dtype=ckpt.dtype, **norm)
+    v = unpack(ckpt.v, ckpt.dtype)
     out = chunk_bwd(qn.view(B, T, H, dk), kn.view(B, T, H, dk), v.view(B, T, H, dv), g, beta, d_o,
-                    initial_state, cu_seqlens, d_final_state, workspace, stream, exact)
+                    initial_state, cu_seqlens, d_final_state, workspace, None, exact)
     raw = qk_norm_rope_bwd(out["dq"].view(B * T, H, dk), out["dk"].view(B * T, H, dk), ckpt.q, ckpt.k,
-                           dtype=ckpt.dtype, stream=stream, **norm)
+                           dtype=ckpt.dtype, **norm)
     out.update(dq=raw["dq"].view(B, T, H, dk), dk=raw["dk"].view(B, T, H, dk), dw_q=raw["dw_q"],
                dw_k=raw["dw_k"])
     return out

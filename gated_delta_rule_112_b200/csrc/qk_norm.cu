@@ -919,9 +919,12 @@ int check_params(const gdn_qk_params *p) {
   return GDN_OK;
 }
 
-bool rows_ok(const gdn_rows *r, int H, int d, size_t e) {
-  return r && r->data && aligned(r->data, e) && r->head_stride >= d && r->head_stride < (1 << 28) &&
-         r->token_stride >= (H > 0 ? int64_t(H - 1) * r->head_stride + d : 0);
+// Rows that do not overlap, token by token or head by head.
+bool rows_ok(const gdn_rows *r, int T, int H, int d, size_t e) {
+  if (!r || !r->data || !aligned(r->data, e)) return false;
+  const int64_t ts = r->token_stride, hs = r->head_stride;
+  if (ts < d || hs < d || hs >= (1 << 28)) return false;
+  return ts >= int64_t(H - 1) * hs + d || hs >= int64_t(T - 1) * ts + d;
 }
 
 int fill(QkArgs &A, const gdn_qk_params *p, const gdn_rows *const x[2],
@@ -944,11 +947,11 @@ int fill(QkArgs &A, const gdn_qk_params *p, const gdn_rows *const x[2],
       P.x = x8[i]->codes;
       P.x_scales = x8[i]->scales;
     } else {
-      if (!rows_ok(x[i], P.H, p->d, e)) return GDN_ERR_INVALID_ARG;
+      if (!rows_ok(x[i], p->T, P.H, p->d, e)) return GDN_ERR_INVALID_ARG;
       P.x = x[i]->data; P.x_ts = x[i]->token_stride * e; P.x_hs = int(x[i]->head_stride * e);
     }
     if (dy) {
-      if (!rows_ok(dy[i], P.H, p->d, dye)) return GDN_ERR_INVALID_ARG;
+      if (!rows_ok(dy[i], p->T, P.H, p->d, dye)) return GDN_ERR_INVALID_ARG;
       P.dy = dy[i]->data; P.dy_ts = dy[i]->token_stride * dye; P.dy_hs = int(dy[i]->head_stride * dye);
     }
     if (out8 && out8[i] && out8[i]->codes) {
@@ -957,7 +960,7 @@ int fill(QkArgs &A, const gdn_qk_params *p, const gdn_rows *const x[2],
       P.scales = out8[i]->scales;
     }
     if (out[i] && out[i]->data) {
-      if (!rows_ok(out[i], P.H, p->d, e)) return GDN_ERR_INVALID_ARG;
+      if (!rows_ok(out[i], p->T, P.H, p->d, e)) return GDN_ERR_INVALID_ARG;
       P.out = out[i]->data; P.out_ts = out[i]->token_stride * e; P.out_hs = int(out[i]->head_stride * e);
     } else if (!P.codes) {
       return GDN_ERR_INVALID_ARG;

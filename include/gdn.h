@@ -458,8 +458,9 @@ int gdn_recurrent_fwd(const void *q, const void *k, const void *v, const float *
 #define GDN_NORM_RMS  2
 
 /* Rows of T tokens' heads in device memory, strides in elements: element e of
- * head h of token t at data[t * token_stride + h * head_stride + e]. Aligned to
- * its element size; whole 16-byte rows are read fastest. */
+ * head h of token t at data[t * token_stride + h * head_stride + e], tokens or
+ * heads outermost, rows not overlapping, head_stride below 2^28. Aligned to the
+ * element size; rows and strides of whole 16-byte pieces are read fastest. */
 typedef struct {
   void *data;
   int64_t token_stride, head_stride;

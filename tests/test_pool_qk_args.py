@@ -82,7 +82,8 @@ def test_norm_refuses_parameters(L, bad):
 def test_norm_refuses_rows(L):
     good, p = ctypes.byref(rows()), ctypes.byref(params())
     k8 = ctypes.byref(gdn._PackedRows(1 << 20, 1 << 20))
-    for bad in (rows(None), rows((1 << 20) + 1), rows(hs=127), rows(ts=255)):
+    for bad in (rows(None), rows((1 << 20) + 1), rows(hs=127), rows(ts=255), rows(ts=128, hs=511),
+                rows(ts=1 << 40, hs=1 << 28)):
         b = ctypes.byref(bad)
         assert L.gdn_qk_norm_rope_fwd(p, b, good, good, good, None, None, None) == gdn.ERR_INVALID_ARG
         assert L.gdn_qk_norm_rope_fwd(p, good, good, good, b, None, None, None) == gdn.ERR_INVALID_ARG

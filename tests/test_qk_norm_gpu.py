@@ -279,6 +279,25 @@ def test_strided_unaligned_and_in_place():
                 assert torch.equal(g3[n], g1[n])
 
 
+def test_heads_outermost():
+    """[H, T, d] in memory, as a batch of heads: read, written and taken back through without a copy."""
+    import gated_delta_rule_112_b200 as gdn
+    q, k, w, how = make(37, 3, 2, 128, BF, 128, "rms", True, seed=61)
+    ref = gdn.qk_norm_rope_fwd(q.cuda(), k.cuda(), pack=True, **dev(how, w))
+    a, b = (x.cuda().transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k))
+    y = gdn.qk_norm_rope_fwd(a, b, pack=True, **dev(how, w))
+    for i in range(2):
+        assert torch.equal(y[i], ref[i])
+        assert torch.equal(y[2 + i].codes.view(torch.uint8), ref[2 + i].codes.view(torch.uint8))
+    out = tuple(torch.empty(x.shape[1], 37, 128, dtype=BF, device="cuda").transpose(0, 1) for x in (q, k))
+    gdn.qk_norm_rope_fwd(a, b, out=out, **dev(how, w))
+    assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+    dy = [torch.randn(x.shape, generator=torch.Generator().manual_seed(4)).cuda() for x in (q, k)]
+    g = gdn.qk_norm_rope_bwd(*dy, a, b, **dev(how, w))
+    want = gdn.qk_norm_rope_bwd(*dy, q.cuda(), k.cuda(), **dev(how, w))
+    assert all(torch.equal(g[n], want[n]) for n in want)
+
+
 def test_far_positions_keep_their_angles():
     """Positions up to 2^31 - 1 and negative ones: fp32 accuracy of the rotation, whatever the turns."""
     import gated_delta_rule_112_b200 as gdn
