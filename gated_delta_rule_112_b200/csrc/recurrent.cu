@@ -366,6 +366,8 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
     if (warp < n2)
       fetch<T, KDA>(A, t0 + int64_t(p2) + warp, h, hk, col0, lane, sm.rows[b & 1], sm.v[slot2], warp);
     const RecCoef<KDA> &C = sm.coef[b & 1];
+    if (b) __syncthreads();           // the next group's rows have landed
+    if (n1 > 0) relate<KDA>(sm.rows[(b + 1) & 1], sm.coef[(b + 1) & 1], warp, n1, lane);
 
 #pragma unroll 1
     for (int m = 0; m < n0; ++m) {
@@ -423,9 +425,6 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
           sm.ue[m][c] = KDA ? u[m] : C.e[m] * u[m];
         }
       }
-    } else if (n1 > 0) {              // meanwhile: the next group's tokens, two a warp
-      relate<KDA>(sm.rows[(b + 1) & 1], sm.coef[(b + 1) & 1], 2 * (warp & 1), n1, lane);
-      relate<KDA>(sm.rows[(b + 1) & 1], sm.coef[(b + 1) & 1], 2 * (warp & 1) + 1, n1, lane);
     }
     __syncthreads();
 
