@@ -27,6 +27,16 @@
 // 2 pi in fp64, less its whole turns, so far positions lose nothing; fp32 sine
 // and cosine of the remainder follow.
 //
+// Measured (B200, 16384 tokens, 16 + 16 heads of d = 128, bf16): forward 46 us =
+// 89 % of the copy rate, gradients from fp32 ones 95 us = 86 %, forward with the
+// checkpoint 71 us = 72 %, gradients with weights from the checkpoint 103 us = 70
+// %. The first two wait for HBM; the 8-bit ones issue two to three instructions
+// an element pair and are bound by both. What brought them there from 83, 128,
+// 117 and 140 us: a pair's elements in one lane (no exchange), factors formed
+// once a token, paired multiply-adds, sixteen elements a lane, reads without
+// conditions. Two CTAs of 128 registers a thread an SM, with four rows a lane in
+// flight: three CTAs of 80 with two were slower (89 us with the checkpoint).
+//
 // Checkpoint: 32 consecutive elements of a row share a power of two 2^e, the
 // smallest (e >= -127) with max|x| <= 448 * 2^e over the block's finite
 // elements, and are stored as e4m3 of x 2^-e (to nearest even); an element that

@@ -25,8 +25,14 @@
 // r < 4, p < d_k / 32). The two sub lanes add up their X and Y by a shuffle,
 // the four warps through shared memory; then one thread has a column's X of
 // every token and another its Y, which makes the chain over a group's tokens
-// two barriers long. (With all rows of 16 columns in one warp and three
-// shuffles instead, two tokens a pass, 64 tokens of one state took 39 us.)
+// two barriers long. Measured (B200, 64 runs of 1 to 6 tokens, 32 heads, d =
+// 128): 50 us, 64 % of the copy rate; with all rows of 16 columns in one warp,
+// three shuffles and two tokens a pass instead, 56 us. One state's 64 tokens
+// alone take 42 us (39 us that way): a warp then has its scheduler to itself
+// and waits for its own operands. Short runs are bound by the chain from a
+// CTA's slot to its rows to its state, which four CTAs an SM overlap; long ones
+// by the multiply-adds and the instructions around them (313 a token and warp,
+// 96 of them paired multiply-adds).
 //
 // k, q, v and the decays of a group come through shared memory in fp32, a token
 // a warp: the rows of the group after next are on their way from HBM, those of
@@ -492,6 +498,8 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
 // of rows) and the warps' partial x and y meet in shared memory. The token's
 // rows and gates do not depend on the slot and are under way while it is read;
 // so is the search for a second run with the same slot while the state is.
+// Bound by HBM: 256 states of 32 heads, d = 128, in 170 us = 97 % of the copy
+// rate; 96 x 32 bf16 states with the channel gate in 34 us = 93 %.
 // 16 pieces a lane either way: 8 warps for an fp32 state, 4 for a bf16 one (8
 // there too where rows and columns are checked, which takes registers).
 template <typename ST, bool FULL>
@@ -694,7 +702,9 @@ cudaError_t launch_np(RecArgs &A, cudaStream_t s) {
 
 template <typename T, typename ST, bool KDA>
 cudaError_t launch_gate(RecArgs &A, cudaStream_t s) {
-  // One token a run goes to its own kernel, where the rows come in whole pieces.
+  // One token a run goes to its own kernel, where the rows come in whole pieces
+  // (170 us against 211 us for 256 x 32 fp32 states, 34 us against 64 us for 96
+  // x 32 bf16 ones by the kernel for runs).
   if (!A.cu && A.L == 1 && A.dv % Piece<ST>::n == 0) {
     const dim3 units = grid_of(A, A.Hv);
     if (A.dk == 128 && A.dv == 128)
