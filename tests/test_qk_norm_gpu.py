@@ -311,6 +311,23 @@ def test_far_positions_keep_their_angles():
         assert_close(f"position {int(pos[t])}", np64(y[t]), ref[t].numpy(), TOL_F32)
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements (and 2^32 bytes): the last token's rows, and the codes of them."""
+    import gated_delta_rule_112_b200 as gdn
+    T, d = 8_500_000, 256
+    x = torch.empty(T, 1, d, dtype=BF, device="cuda")
+    last = torch.randn(3, 1, d, generator=torch.Generator().manual_seed(8)).to(BF)
+    x[-3:] = last.cuda()
+    y, _, p, _ = gdn.qk_norm_rope_fwd(x, None, norm="rms", pack=True)
+    assert_close("y", np64(y[-3:]), plain(last, None, dict(norm="rms")).numpy(), tol(BF))
+    codes, scales = plain_pack(last)
+    assert torch.equal(p.scales[-3:].cpu(), scales) and torch.equal(p.codes[-3:].cpu().double(), codes)
+    del y
+    out = gdn.qk_norm_rope_bwd(x, None, p, None, norm="rms")
+    ref, _ = grads_of(value(gdn.Packed(p.codes[-3:], p.scales[-3:])), None, dict(norm="rms"), 1.0, last)
+    assert_close("dx", np64(out["dq"][-3:]), ref, tol(BF))
+
+
 def test_rows_of_zeros_and_of_infinities():
     import gated_delta_rule_112_b200 as gdn
     q = torch.zeros(3, 2, 128)
@@ -330,6 +347,10 @@ def test_no_tokens_and_one_tensor():
     assert y[0].shape == (0, 2, 64)
     out = gdn.qk_norm_rope_bwd(q.cuda(), k.cuda(), q.cuda(), k.cuda(), **dev(how, w))
     assert torch.equal(out["dw_q"].cpu(), torch.zeros(64)) and torch.equal(out["dw_k"].cpu(), torch.zeros(64))
+    q, k, w, how = make(4, 2, 0, 64, BF, 32, "rms", True)                   # no heads of k
+    y = gdn.qk_norm_rope_fwd(q.cuda(), k.cuda(), **dev(how, w))
+    assert y[1].shape == (4, 0, 64)
+    assert_close("q", np64(y[0]), plain(q, w[0], how).numpy(), tol(BF))
     q, k, w, how = make(5, 2, 1, 64, BF, 32, "rms", True)
     both = gdn.qk_norm_rope_fwd(q.cuda(), k.cuda(), **dev(how, w))
     one = gdn.qk_norm_rope_fwd(q.cuda(), None, **{**dev(how, w), "w_k": None})

@@ -137,10 +137,10 @@ def test_equal_lengths_without_cu_and_without_slots():
 
 def test_matches_decode_step():
     import gated_delta_rule_112_b200 as gdn
-    for channel in (False, True):
+    for channel, cu in ((False, False), (True, False), (False, True), (True, True)):
         d = make([1] * 6, 3, 3, 128, 128, F, seed=22, channel=channel, spare=0)
         d["slots"] = torch.arange(6, dtype=torch.int32)
-        o, pool = call(d)
+        o, pool = call(d, cu=cu)
         state = d["pool"].cuda()
         step = gdn.kda_decode_step if channel else gdn.decode_step
         ref = step(*(d[x].cuda() for x in ("q", "k", "v", "g", "beta")), state)
@@ -197,6 +197,10 @@ def test_strided_and_unaligned_inputs():
             o = gdn.recurrent_fwd(q, k, v, d["g"].cuda(), d["beta"].cuda(), pool, d["slots"].cuda(),
                                   d["cu"].cuda())
             check(d, o, pool)
+            one = make([1] * T, 2, 4, 128, 64, dtype, seed=35)     # the same rows, one token a run
+            pool = one["pool"].cuda()
+            o = gdn.recurrent_fwd(q, k, v, d["g"].cuda(), d["beta"].cuda(), pool, one["slots"].cuda())
+            check({**one, **{x: d[x] for x in ("q", "k", "v", "g", "beta")}}, o, pool)
 
 
 @pytest.mark.parametrize("channel", [False, True])
@@ -211,6 +215,111 @@ def test_gates_at_their_ends(channel):
     check(d, o, pool)
 
 
+# One token a run without boundaries has a kernel of its own.
+ONE = [
+    # N, Hk, Hv, dk, dv, dtype, pool dtype, channel gate
+    (1, 1, 1, 128, 128, BF, F, False),
+    (5, 2, 6, 128, 128, BF, F, True),
+    (7, 3, 3, 128, 128, F, BF, False),
+    (4, 2, 4, 128, 128, BF, BF, True),
+    (3, 1, 2, 96, 80, BF, F, False),
+    (3, 1, 2, 100, 72, F, BF, True),
+    (2, 2, 2, 33, 8, BF, BF, False),
+    (2, 1, 5, 64, 12, F, F, True),
+    (2, 1, 1, 128, 12, F, BF, False),          # rows of a bf16 state that are no whole pieces
+    (3, 1, 1, 1, 4, F, F, False),
+]
+
+
+@pytest.mark.parametrize("case", range(len(ONE)))
+def test_one_token_a_run(case):
+    N, Hk, Hv, dk, dv, dtype, pdt, channel = ONE[case]
+    d = make([1] * N, Hk, Hv, dk, dv, dtype, pdt, channel, seed=100 + case, beta_scale=2.0)
+    o, pool = call(d, cu=False)
+    check(d, o, pool)
+    others = sorted(set(range(d["pool"].shape[0])) - set(d["slots"].tolist()))
+    assert torch.equal(pool[others].cpu(), d["pool"][others])
+
+
+@pytest.mark.parametrize("pdt", [F, BF])
+@pytest.mark.parametrize("channel", [False, True])
+def test_one_token_keep_reset_padding_and_decay_of_zero(pdt, channel):
+    d = make([1] * 6, 2, 4, 128, 128, BF, pdt, channel, seed=120)
+    d["g"][2] = float("-inf")
+    keep, reset = [1, 0, 1, 1, 0, 1], [False, False, False, True, True, False]
+    slots = d["slots"].tolist()
+    slots[5] = -3
+    out = torch.full(tuple(d["v"].shape), 7.0, dtype=BF, device="cuda")
+    o, pool = call(d, keep=keep, reset=reset, slots=slots, cu=False, out=out)
+    assert torch.equal(o[5].cpu(), torch.full_like(o[5].cpu(), 7.0))
+    ro, rp = reference(d, keep=keep, reset=reset, slots=slots)
+    assert_close("o", np64(o[:5]), ro[:5], tol(BF))
+    assert_close("pool", np64(pool), rp, tol(pdt))
+    for n in (1, 4):
+        assert torch.equal(pool[slots[n]].cpu(), d["pool"][slots[n]])
+
+
+@pytest.mark.parametrize("how,spoilt", [
+    (dict(slots=[0, 99, 2]), [1]), (dict(slots=[0, 2, 2]), [1, 2]),
+    (dict(slots=[0, 2, 2], keep=[1, 0, 1]), [1, 2]), (dict(keep=[1, 2, 1]), [1]),
+    (dict(keep=[1, -1, 1]), [1]), (dict(slots=[0, 2, 2], keep=[1, 0, 0]), [])])
+def test_one_token_bad_runs(how, spoilt):
+    import gated_delta_rule_112_b200 as gdn
+    d = make([1] * 3, 1, 2, 128, 128, BF, seed=121)
+    d["slots"] = torch.arange(3, dtype=torch.int32)
+    status = gdn.status_block()
+    o, pool = call(d, status=status, cu=False, **how)
+    assert gdn.get_status(status) == (gdn.ERR_INVALID_ARG if spoilt else gdn.OK)
+    slots = how.get("slots", [0, 1, 2])
+    ro, rp = reference(d, slots=[-1 if n in spoilt else x for n, x in enumerate(slots)],
+                       keep=None if "keep" not in how else
+                       [0 if n in spoilt else x for n, x in enumerate(how["keep"])])
+    for n in range(3):
+        if n in spoilt:
+            assert torch.isnan(o[n]).all()
+        else:
+            assert_close(f"o of run {n}", np64(o[n]), ro[n], tol(BF))
+    assert_close("pool", np64(pool), rp, TOL_F32)
+
+
+@pytest.mark.parametrize("cu", [False, True])
+def test_more_runs_than_a_grid_dimension(cu):
+    """70,000 runs of a tiny state; the last ones checked against the rule in fp64."""
+    import gated_delta_rule_112_b200 as gdn
+    N = 70_000
+    d = make([1] * N, 1, 1, 4, 4, F, seed=122, spare=0)
+    status = gdn.status_block()
+    o, pool = call(d, cu=cu, status=status)
+    assert gdn.get_status(status) == gdn.OK
+    q, k, v, g, b = (np64(d[x])[:, 0] for x in ("q", "k", "v", "g", "beta"))
+    S = np64(d["pool"])[d["slots"].numpy(), 0] * np.exp(g)[:, None, None]
+    u = b[:, None] * (v - np.einsum("nji,nj->ni", S, k))
+    S = S + k[:, :, None] * u[:, None]
+    assert_close("o", np64(o[:, 0]), np.einsum("nji,nj->ni", S, q), TOL_F32)
+    assert_close("pool", np64(pool[d["slots"].long().cuda(), 0]), S, TOL_F32)
+
+
+def test_two_calls_at_once_on_disjoint_slots():
+    import gated_delta_rule_112_b200 as gdn
+    d = make([3, 5, 2, 7], 2, 4, 128, 128, BF, seed=123)
+    ref, rpool = call(d)
+    pool = d["pool"].cuda()
+    args = [d[x].cuda() for x in ("q", "k", "v", "g", "beta")]
+    outs = []
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for rep in range(2):
+        lo, hi = (0, 8) if rep == 0 else (8, 17)
+        cu = ints([0, 3, 8] if rep == 0 else [0, 2, 9])
+        slots = d["slots"][2 * rep:2 * rep + 2].cuda()
+        part = [x[lo:hi].contiguous() for x in args]
+        torch.cuda.synchronize()
+        outs.append((part, slots, cu))
+    os = [gdn.recurrent_fwd(*p, pool, s, c, stream=st) for (p, s, c), st in zip(outs, streams)]
+    torch.cuda.synchronize()
+    assert torch.equal(torch.cat(os), ref) and torch.equal(pool, rpool)
+
+
 def test_large_pool_offsets():
     """Slots whose elements lie past 2^32 bytes and past 2^31 elements."""
     import gated_delta_rule_112_b200 as gdn
@@ -221,6 +330,11 @@ def test_large_pool_offsets():
     pool[slots] = d["pool"].cuda()
     o = gdn.recurrent_fwd(*(d[x].cuda() for x in ("q", "k", "v", "g", "beta")), pool, ints(slots),
                           d["cu"].cuda())
+    d["slots"] = torch.arange(2, dtype=torch.int32)
+    check(d, o, pool[slots])
+    d = make([1, 1], 1, 1, 128, 128, BF, BF, seed=34, spare=0)             # one token a run
+    pool[slots] = d["pool"].cuda()
+    o = gdn.recurrent_fwd(*(d[x].cuda() for x in ("q", "k", "v", "g", "beta")), pool, ints(slots))
     d["slots"] = torch.arange(2, dtype=torch.int32)
     check(d, o, pool[slots])
 
@@ -321,5 +435,6 @@ def test_captured_replayed_and_on_another_stream():
 def test_workload_pool_step_full_size():
     """The decode workload's batch (N=256, H=32, d=128) from a pool, every state and output."""
     d = make([1] * 256, 32, 32, 128, 128, BF, seed=33, spare=8)
-    o, pool = call(d)
-    check(d, o, pool)
+    for cu in (False, True):
+        o, pool = call(d, cu=cu)
+        check(d, o, pool)
