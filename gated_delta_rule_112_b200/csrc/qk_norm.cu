@@ -28,7 +28,7 @@
 // and cosine of the remainder follow.
 //
 // Measured (B200, 16384 tokens, 16 + 16 heads of d = 128, bf16): forward 46 us =
-// 89 % of the copy rate, gradients from fp32 ones 95 us = 86 %, forward with the
+// 89 % of the copy rate, gradients from fp32 ones 91 us = 90 %, forward with the
 // checkpoint 71 us = 72 %, gradients with weights from the checkpoint 103 us = 70
 // %. The first two wait for HBM; the 8-bit ones issue two to three instructions
 // an element pair and are bound by both. What brought them there from 83, 128,
@@ -50,9 +50,13 @@
 namespace gdn {
 namespace {
 
-constexpr int kQkThreads = 256, kQkWarps = kQkThreads / 32;
+constexpr int kQkThreads = 256;
 constexpr int kMaxD = 256;
-constexpr int kFwdBlocksPerSm = 2, kBwdBlocksPerSm = 2;
+constexpr int kBlocksPerSm = 2;
+// Gradients without weights hold fewer values a row: five CTAs of four warps an
+// SM (102 registers a thread) instead of two of eight, 91 us against 95 us for
+// 16384 x 32 rows. The other kernels lose by it (forward 46 -> 52 us).
+constexpr int kPlainBwdThreads = 128, kPlainBwdBlocksPerSm = 5;
 
 // How the pairs lie. Split: halves in chunks of four; shared: any halves.
 enum { kPairNone, kPairInterleaved, kPairSplit, kPairShared };
@@ -440,9 +444,9 @@ __device__ __forceinline__ float rnorm(const QkArgs &A, float ss) {
 }
 
 // (w + w0) * scale of q's and of k's elements, 1 * scale without weights.
-template <typename T>
+template <typename T, int THREADS>
 __device__ __forceinline__ void stage_weights(const QkArgs &A, bool scaled, bool weighted, float (*w)[kMaxD]) {
-  for (int i = threadIdx.x; i < 2 * kMaxD; i += kQkThreads) {
+  for (int i = threadIdx.x; i < 2 * kMaxD; i += THREADS) {
     const Part &P = A.p[i / kMaxD];
     const int e = i % kMaxD;
     float x = 1.f;
@@ -626,21 +630,21 @@ __device__ __forceinline__ Item item_at(const QkArgs &A, int64_t item) {
 // PACK: also write codes.
 constexpr int kFwdE = 8, kBwdE = 4;
 template <typename T, bool PACKED, bool PACK, int PAIR, int ACC, int LG>
-__global__ void __launch_bounds__(kQkThreads, kFwdBlocksPerSm) gdn_qk_fwd_kernel(const __grid_constant__ QkArgs A) {
-  constexpr int E = kFwdE, U = 4;
+__global__ void __launch_bounds__(kQkThreads, kBlocksPerSm) gdn_qk_fwd_kernel(const __grid_constant__ QkArgs A) {
+  constexpr int E = kFwdE, U = 4, kWarps = kQkThreads / 32;
   __shared__ __align__(16) float w_all[2][kMaxD];
-  __shared__ __align__(16) float cs_all[PAIR == kPairNone ? 1 : kQkWarps][kMaxD];
-  __shared__ __align__(16) float rows_all[PAIR == kPairShared ? kQkWarps : 1][2 * kMaxD];
-  __shared__ uint32_t tops_all[PACK && PAIR == kPairSplit ? kQkWarps * 64 : 1];
+  __shared__ __align__(16) float cs_all[PAIR == kPairNone ? 1 : kWarps][kMaxD];
+  __shared__ __align__(16) float rows_all[PAIR == kPairShared ? kWarps : 1][2 * kMaxD];
+  __shared__ uint32_t tops_all[PACK && PAIR == kPairSplit ? kWarps * 64 : 1];
   const int lg = LG ? LG : A.lg, G = 1 << lg, R = 32 >> lg;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> lg, l = lane & (G - 1);
   float *cs = cs_all[PAIR == kPairNone ? 0 : warp];
   float *row_buf = rows_all[PAIR == kPairShared ? warp : 0] + (lane & -G) * 2 * E;
   uint32_t *tops = tops_all + (PACK && PAIR == kPairSplit ? warp * 64 + sub * 8 : 0);
   const Lane L = lane_place<E, PAIR>(A, l);
-  stage_weights<T>(A, true, true, w_all);
-  const int64_t nwarps = int64_t(gridDim.x) * kQkWarps, items = int64_t(A.T) * A.splits;
-  for (int64_t item = int64_t(blockIdx.x) * kQkWarps + warp; item < items; item += nwarps) {
+  stage_weights<T, kQkThreads>(A, true, true, w_all);
+  const int64_t nwarps = int64_t(gridDim.x) * kWarps, items = int64_t(A.T) * A.splits;
+  for (int64_t item = int64_t(blockIdx.x) * kWarps + warp; item < items; item += nwarps) {
     const Item I = item_at(A, item);
     if (PAIR != kPairNone) make_angles(A, I.t, lane, E << lg, cs);
     for (int part = 0; part < 2; ++part) {
@@ -695,24 +699,26 @@ __global__ void __launch_bounds__(kQkThreads, kFwdBlocksPerSm) gdn_qk_fwd_kernel
 
 // WEIGHTS: weights and their gradients.
 template <typename T, typename DT, bool PACKED, bool WEIGHTS, int PAIR, int ACC, int LG>
-__global__ void __launch_bounds__(kQkThreads, kBwdBlocksPerSm) gdn_qk_bwd_kernel(const __grid_constant__ QkArgs A) {
-  constexpr int E = kBwdE, U = 2;
+__global__ void __launch_bounds__(WEIGHTS ? kQkThreads : kPlainBwdThreads,
+                                  WEIGHTS ? kBlocksPerSm : kPlainBwdBlocksPerSm)
+    gdn_qk_bwd_kernel(const __grid_constant__ QkArgs A) {
+  constexpr int E = kBwdE, U = 2, kThreads = WEIGHTS ? kQkThreads : kPlainBwdThreads, kWarps = kThreads / 32;
   constexpr bool kWhole = ACC >= E;
   __shared__ __align__(16) float w_all[2][kMaxD], one[2][kMaxD];
-  __shared__ __align__(16) float cs_all[PAIR == kPairNone ? 1 : kQkWarps][kMaxD];
-  __shared__ __align__(16) float rows_all[PAIR == kPairShared || WEIGHTS ? kQkWarps : 1][kMaxD];
+  __shared__ __align__(16) float cs_all[PAIR == kPairNone ? 1 : kWarps][kMaxD];
+  __shared__ __align__(16) float rows_all[PAIR == kPairShared || WEIGHTS ? kWarps : 1][kMaxD];
   const int lg = LG ? LG : A.lg, G = 1 << lg, R = 32 >> lg;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> lg, l = lane & (G - 1);
   float *cs = cs_all[PAIR == kPairNone ? 0 : warp];
   float *row_buf = rows_all[PAIR == kPairShared || WEIGHTS ? warp : 0] + (lane & -G) * 2 * E;
   const Lane L = lane_place<E, PAIR>(A, l);
-  if (WEIGHTS) stage_weights<T>(A, false, true, w_all);
-  stage_weights<T>(A, true, false, one);
-  const int64_t nwarps = int64_t(gridDim.x) * kQkWarps, items = int64_t(A.T) * A.splits;
+  if (WEIGHTS) stage_weights<T, kThreads>(A, false, true, w_all);
+  stage_weights<T, kThreads>(A, true, false, one);
+  const int64_t nwarps = int64_t(gridDim.x) * kWarps, items = int64_t(A.T) * A.splits;
   Row<E> dw[2];
 #pragma unroll
   for (int i = 0; i < 2 * E; ++i) dw[i / E].v[i % E] = pair(0.f, 0.f);
-  for (int64_t item = int64_t(blockIdx.x) * kQkWarps + warp; item < items; item += nwarps) {
+  for (int64_t item = int64_t(blockIdx.x) * kWarps + warp; item < items; item += nwarps) {
     const Item I = item_at(A, item);
     if (PAIR != kPairNone) make_angles(A, I.t, lane, E << lg, cs);
 #pragma unroll
@@ -792,9 +798,9 @@ __global__ void __launch_bounds__(kQkThreads, kBwdBlocksPerSm) gdn_qk_bwd_kernel
         if (e < A.d) row_buf[e] = i & 1 ? f.y : f.x;
       }
       __syncthreads();
-      for (int e = threadIdx.x; e < A.d; e += kQkThreads) {
+      for (int e = threadIdx.x; e < A.d; e += kThreads) {
         float s = 0.f;
-        for (int i = 0; i < kQkWarps * R; ++i) s += rows_all[i / R][(i % R) * G * 2 * E + e];
+        for (int i = 0; i < kWarps * R; ++i) s += rows_all[i / R][(i % R) * G * 2 * E + e];
         A.dw_part[(int64_t(part) * gridDim.x + blockIdx.x) * A.d + e] = s;
       }
     }
@@ -849,15 +855,15 @@ int pair_mode(const gdn_qk_params *p, int acc, int e) {
 // Rows an item and items a token: whole tokens, whose cosines then serve every
 // head, where there are enough of them for all warps; else fewer rows, down to
 // one step of a warp.
-unsigned plan(QkArgs &A, int e, int per_sm) {
+unsigned plan(QkArgs &A, int e, int threads, int per_sm) {
   for (A.lg = 2; (2 * e) << A.lg < A.d; ++A.lg) {}
   const int rows = A.p[0].H + A.p[1].H, step = 32 >> A.lg, sms = device_sms();
-  const int64_t warps = int64_t(sms > 0 ? sms : 1) * per_sm * kQkWarps;
+  const int64_t warps = int64_t(sms > 0 ? sms : 1) * per_sm * (threads / 32);
   int64_t want = (int64_t(A.T) * rows + warps - 1) / warps;          // rows a warp
   want = (want + step - 1) / step * step;
   A.rpi = int(want < 1 ? 1 : want < rows ? want : rows > 0 ? rows : 1);
   A.splits = (rows + A.rpi - 1) / A.rpi;
-  const int64_t blocks = (int64_t(A.T) * A.splits + kQkWarps - 1) / kQkWarps;
+  const int64_t blocks = (int64_t(A.T) * A.splits + threads / 32 - 1) / (threads / 32);
   const int64_t most = int64_t(sms > 0 ? sms : 1) * per_sm;
   return unsigned(blocks < 1 ? 1 : blocks < most ? blocks : most);
 }
@@ -906,7 +912,7 @@ cudaError_t bwd_launch(const QkArgs &A, int dtype, int grad_dtype, int pair, int
     using DT = decltype(grad);
     with_variant<kBwdE>(pair, acc, A.lg, [&](auto p, auto a, auto g) {
       gdn_qk_bwd_kernel<T, DT, PACKED, WEIGHTS, decltype(p)::value, decltype(a)::value, decltype(g)::value>
-          <<<grid, kQkThreads, 0, s>>>(A);
+          <<<grid, WEIGHTS ? kQkThreads : kPlainBwdThreads, 0, s>>>(A);
     });
   };
   if (dtype == GDN_F32) go(float{}, float{});
@@ -989,7 +995,7 @@ int run_fwd(const gdn_qk_params *p, const gdn_rows *const x[2], const gdn_packed
   if (rc != GDN_OK) return rc;
   if (!A.p[0].H && !A.p[1].H) return GDN_OK;
   const bool pack = A.p[0].codes || A.p[1].codes;
-  const unsigned grid = plan(A, kFwdE, kFwdBlocksPerSm);
+  const unsigned grid = plan(A, kFwdE, kQkThreads, kBlocksPerSm);
   const int acc = access_width(A, p->dtype == GDN_BF16 ? 2 : 4, 2, PACKED);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int pair = pair_mode(p, acc, kFwdE);
@@ -1016,7 +1022,8 @@ int run_bwd(const gdn_qk_params *p, const gdn_rows *const dy[2], int grad_dtype,
   rc = fill(A, p, x, PACKED ? x8 : nullptr, dy, grad_dtype == GDN_BF16 ? 2 : 4, out, nullptr);
   if (rc != GDN_OK) return rc;
   A.dw_part = static_cast<float *>(ws);
-  const unsigned grid = plan(A, kBwdE, kBwdBlocksPerSm);
+  const unsigned grid = dw_q || dw_k ? plan(A, kBwdE, kQkThreads, kBlocksPerSm)
+                                     : plan(A, kBwdE, kPlainBwdThreads, kPlainBwdBlocksPerSm);
   const int acc = access_width(A, p->dtype == GDN_BF16 ? 2 : 4, grad_dtype == GDN_BF16 ? 2 : 4, PACKED);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!A.p[0].H && !A.p[1].H && !dw_q && !dw_k) return GDN_OK;
@@ -1056,7 +1063,7 @@ int gdn_qk_norm_rope_fwd_packed(const gdn_qk_params *p, const gdn_packed *q, con
 
 size_t gdn_qk_norm_rope_bwd_workspace_size(const gdn_qk_params *p) {
   if (check_params(p) != GDN_OK || (!p->w_q && !p->w_k)) return 0;
-  return align_up(size_t(2) * device_sms() * kBwdBlocksPerSm * p->d * sizeof(float), 256);
+  return align_up(size_t(2) * device_sms() * kBlocksPerSm * p->d * sizeof(float), 256);
 }
 
 int gdn_qk_norm_rope_bwd(const gdn_qk_params *p, const gdn_rows *dq_out, const gdn_rows *dk_out,
