@@ -58,7 +58,7 @@ constexpr int kBlocksPerSm = 2;
 // 16384 x 32 rows. The other kernels lose by it (forward 46 -> 52 us).
 constexpr int kPlainBwdThreads = 128, kPlainBwdBlocksPerSm = 5;
 
-// How the pairs lie. Split: halves in chunks of four; shared: any halves.
+// How the pairs lie. Split: halves that fall into chunks; shared: any halves.
 enum { kPairNone, kPairInterleaved, kPairSplit, kPairShared };
 
 struct Part {                     // q or k
