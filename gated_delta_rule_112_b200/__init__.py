@@ -388,7 +388,8 @@ def recurrent_fwd(q, k, v, g, beta, pool, slots=None, cu_seqlens=None, keep=None
     name = "gdn_recurrent_fwd"
     dev = q.get_device()
     if dev < 0 or stream is not None or dev != torch.cuda.current_device():
-        with _on(name, dev, stream):
+        with _on(name, dev, stream, q, k, v, g, beta, pool, slots, cu_seqlens, keep, reset, out,
+                 status):
             return recurrent_fwd(q, k, v, g, beta, pool, slots, cu_seqlens, keep, reset, out, status)
     T, Hk, dk = q.shape
     _, Hv, dv = v.shape
@@ -440,15 +441,24 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 
 
 @contextlib.contextmanager
-def _on(name, dev, stream):
+def _on(name, dev, stream, *used):
     """The tensors' device and the caller's stream as the current ones: outputs
-    are allocated on the stream that writes them."""
+    are allocated on the stream that writes them, and the memory of what the
+    call uses is not given away before that stream has run it."""
     if dev < 0:
         raise ValueError(f"{name}: all tensors must be CUDA tensors")
     if stream is not None and stream.device_index != dev:
         raise ValueError(f"{name}: the stream is on device {stream.device_index}, the tensors on {dev}")
     with torch.cuda.device(dev), torch.cuda.stream(stream):
         yield
+    if stream is not None:
+        for t in used:
+            for x in t if isinstance(t, tuple) else (t,):
+                if isinstance(x, tuple):
+                    for y in x:
+                        y.record_stream(stream)
+                elif isinstance(x, torch.Tensor):
+                    x.record_stream(stream)
 
 
 def _at(t):
@@ -574,7 +584,7 @@ def qk_norm_rope_fwd(q, k, w_q=None, w_k=None, positions=None, inv_freq=None, no
     packed, qx, kx = _qk_source(name, q, k)
     dev = qx.get_device()
     if dev < 0 or stream is not None or dev != torch.cuda.current_device():
-        with _on(name, dev, stream):
+        with _on(name, dev, stream, q, k, w_q, w_k, positions, inv_freq, out):
             return qk_norm_rope_fwd(q, k, w_q, w_k, positions, inv_freq, norm, eps, interleaved,
                                     weight_offset, q_scale, rope_scale, pack, dtype, out)
     if packed:
@@ -620,7 +630,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, w_q=None, w_k=None, positions=None, i
     packed, qx, kx = _qk_source(name, q, k)
     dev = qx.get_device()
     if dev < 0 or stream is not None or dev != torch.cuda.current_device():
-        with _on(name, dev, stream):
+        with _on(name, dev, stream, dq_out, dk_out, q, k, w_q, w_k, positions, inv_freq, out,
+                 workspace):
             return qk_norm_rope_bwd(dq_out, dk_out, q, k, w_q, w_k, positions, inv_freq, norm, eps,
                                     interleaved, weight_offset, q_scale, rope_scale, dtype, out,
                                     workspace)
@@ -691,7 +702,8 @@ def chunk_fwd_packed(q, k, v, g, beta, initial_state=None, cu_seqlens=None, chun
     Checkpoint)``; o and the state are those of the exact q, k, v."""
     dev = q.get_device()
     if dev < 0 or stream is not None or dev != torch.cuda.current_device():
-        with _on("chunk_fwd_packed", dev, stream):
+        with _on("chunk_fwd_packed", dev, stream, q, k, v, g, beta, initial_state, cu_seqlens,
+                 *norm.values()):
             return chunk_fwd_packed(q, k, v, g, beta, initial_state, cu_seqlens, chunk,
                                     output_final_state, **norm)
     B, T, H, dk = q.shape
@@ -712,7 +724,8 @@ def chunk_bwd_packed(ckpt: Checkpoint, g, beta, d_o, initial_state=None, cu_seql
     None), dv, dg, dbeta, d_initial_state (fp32)."""
     dev = ckpt.q.codes.get_device()
     if dev < 0 or stream is not None or dev != torch.cuda.current_device():
-        with _on("chunk_bwd_packed", dev, stream):
+        with _on("chunk_bwd_packed", dev, stream, ckpt[:3], g, beta, d_o, initial_state, cu_seqlens,
+                 d_final_state, workspace, *norm.values()):
             return chunk_bwd_packed(ckpt, g, beta, d_o, initial_state, cu_seqlens, d_final_state,
                                     workspace, exact=exact, **norm)
     B, T, H, dk, dv = ckpt.shape

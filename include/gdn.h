@@ -426,8 +426,10 @@ int gdn_chunk_bwd_exact(const void *q, const void *k, const void *v, const float
  * pool, a keep outside [0, length] and tokens outside [0, T] are found on the
  * device: that run's state is left alone, its outputs (unless its tokens are
  * the bad part) are NaN, and the status is GDN_ERR_INVALID_ARG. Runs that keep
- * nothing may share a slot. d_k, d_v <= 128, d_v a multiple of 4. No workspace;
- * the call can be captured, and calls on disjoint slots may overlap.
+ * nothing may share a slot. Boundaries that go backwards make runs overlap:
+ * outputs of the shared tokens are then undefined. d_k, d_v <= 128, d_v a
+ * multiple of 4, H_v < 2^20, N * H_v < 2^30. No workspace; the call can be
+ * captured, and calls on disjoint slots may overlap.
  */
 int gdn_recurrent_fwd(const void *q, const void *k, const void *v, const float *g,
                       const float *beta, void *pool, const int32_t *slots,

@@ -387,6 +387,31 @@ def test_captured_replayed_another_stream_and_repeatable():
         assert all(torch.equal(want[n], out[n]) for n in want)
 
 
+def test_memory_of_another_streams_inputs_is_kept():
+    """Inputs that are given up right after a call on a stream that is still busy: their memory is not handed
+    to the next allocation before the call has read it."""
+    import gated_delta_rule_112_b200 as gdn
+    x = torch.randn(4096, 8, 128, generator=torch.Generator().manual_seed(7)).to(BF)
+    ref = gdn.qk_norm_rope_fwd(x.cuda(), None)[0]
+    busy = torch.randn(6000, 6000, device="cuda")
+    side = torch.cuda.Stream()
+    q = x.cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):                    # some milliseconds of work ahead of the call
+            busy = busy @ busy
+            busy /= busy.norm()
+    y = gdn.qk_norm_rope_fwd(q, None, stream=side)[0]
+    p = gdn.pack(q, stream=side)
+    del q
+    for _ in range(8):
+        torch.empty_like(ref).fill_(float("nan"))
+    z = gdn.unpack(p, stream=side)
+    side.synchronize()
+    assert torch.equal(y, ref)
+    assert torch.equal(z.cpu().double(), value(gdn.pack(x.cuda())))
+
+
 def test_serving_path_together():
     """Projection output -> norms and rotation in place -> the pooled recurrent rule, two calls in a row."""
     import gated_delta_rule_112_b200 as gdn
