@@ -29,7 +29,7 @@
 //
 // Measured (B200, 16384 tokens, 16 + 16 heads of d = 128, bf16): forward 46 us =
 // 89 % of the copy rate, gradients from fp32 ones 91 us = 90 %, forward with the
-// checkpoint 71 us = 72 %, gradients with weights from the checkpoint 103 us = 70
+// checkpoint 67 us = 77 %, gradients with weights from the checkpoint 103 us = 70
 // %. The first two wait for HBM; the 8-bit ones issue two to three instructions
 // an element pair and are bound by both. What brought them there from 83, 128,
 // 117 and 140 us: a pair's elements in one lane (no exchange), factors formed
@@ -530,7 +530,7 @@ __device__ __forceinline__ Top chunk_tops(const Raw<float, E> &r) {
 // Writes the lane's elements in 8 bits. Side by side, 32 / 2E lanes hold a
 // block; with halves in chunks 32 / E lanes' first chunks do, and their second
 // chunks, where rot / 2 is a multiple of 32; for other rot the blocks' maxima
-// meet in shared memory.
+// meet in shared memory. The exponents go to scales, in shared memory too.
 template <typename T, int E, int PAIR, int ACC>
 __device__ __forceinline__ void write_codes(const QkArgs &A, const Rows<uint8_t> &codes, uint8_t *scales,
                                             int h, const Lane &L, bool on, uint32_t *tops,
@@ -608,12 +608,11 @@ __device__ __forceinline__ void write_codes(const QkArgs &A, const Rows<uint8_t>
       if (fabsf(f.y) > 3.402823466e38f) c[i / 2] |= 0x7f00u << (16 * (i & 1));
     }
   }
+  if ((L.a & 31) == 0 && L.na > 0) scales[L.a / 32] = uint8_t(ea);
+  if (PAIR == kPairSplit && (L.b & 31) == 0 && L.nb > 0) scales[L.b / 32] = uint8_t(eb);
   if (!on) return;
   store_codes<E, ACC>(codes.first(h), L.na, c);
   store_codes<E, ACC>(codes.second(h), L.nb, c + E / 4);
-  uint8_t *e = scales + int64_t(h) * ((A.d + 31) / 32);
-  if ((L.a & 31) == 0 && L.na > 0) e[L.a / 32] = uint8_t(ea);
-  if (PAIR == kPairSplit && (L.b & 31) == 0 && L.nb > 0) e[L.b / 32] = uint8_t(eb);
 }
 
 // Where a warp's item lies.
@@ -641,6 +640,10 @@ __global__ void __launch_bounds__(kQkThreads, kBlocksPerSm) gdn_qk_fwd_kernel(co
   float *cs = cs_all[PAIR == kPairNone ? 0 : warp];
   float *row_buf = rows_all[PAIR == kPairShared ? warp : 0] + (lane & -G) * 2 * E;
   uint32_t *tops = tops_all + (PACK && PAIR == kPairSplit ? warp * 64 + sub * 8 : 0);
+  // a step's exponents: R U rows of up to 8 (R halves as a row's lanes double)
+  __shared__ uint8_t scales_all[PACK ? kWarps : 1][64];
+  uint8_t *exps = scales_all[PACK ? warp : 0];
+  const int blocks = (A.d + 31) / 32;
   const Lane L = lane_place<E, PAIR>(A, l);
   stage_weights<T, kQkThreads>(A, true, true, w_all);
   const int64_t nwarps = int64_t(gridDim.x) * kWarps, items = int64_t(A.T) * A.splits;
@@ -659,7 +662,6 @@ __global__ void __launch_bounds__(kQkThreads, kBlocksPerSm) gdn_qk_fwd_kernel(co
       const Rows<T> out(static_cast<T *>(P.out), I.t * P.out_ts, P.out_hs, L, false);
       const int64_t row0 = int64_t(I.t) * P.H;
       const Rows<uint8_t> codes(P.codes, row0 * A.d, A.d, L, false);
-      uint8_t *scales = PACK ? P.scales + row0 * ((A.d + 31) / 32) : nullptr;
       for (int h = h0 + sub; h - sub < h1; h += R * U) {
         typename Src::Data raw[U];
 #pragma unroll
@@ -672,7 +674,9 @@ __global__ void __launch_bounds__(kQkThreads, kBlocksPerSm) gdn_qk_fwd_kernel(co
           unpack(raw[u], x);
           Scales sc = scales_of(raw[u]);
           if constexpr (PACK)
-            if (P.codes) write_codes<T, E, PAIR, ACC>(A, codes, scales, h + u * R, L, on, tops, raw[u], x);
+            if (P.codes)
+              write_codes<T, E, PAIR, ACC>(A, codes, exps + (u * R + sub) * blocks, h + u * R, L, on, tops,
+                                           raw[u], x);
           if (A.norm != GDN_NORM_NONE) {
             const float2 d = dots<E, (ACC >= E)>(L, x, x);
             // (d s) s and not d s^2, which could leave the range where the sum does not
@@ -691,6 +695,15 @@ __global__ void __launch_bounds__(kQkThreads, kBlocksPerSm) gdn_qk_fwd_kernel(co
             store_chunk<E, ACC>(out.first(h + u * R), L.na, x.v);
             store_chunk<E, ACC>(out.second(h + u * R), L.nb, x.v + E / 2);
           }
+        }
+        // consecutive heads' exponents are consecutive bytes: written together
+        // (71 -> 67 us for 16384 x 32 rows, against a byte a lane as they arise)
+        if (PACK && P.codes) {
+          const int h_first = h - sub, bytes = min(R * U, h1 - h_first) * blocks;
+          __syncwarp();
+          for (int i = lane; i < bytes; i += 32)
+            P.scales[(row0 + h_first) * blocks + i] = exps[i];
+          __syncwarp();
         }
       }
     }
