@@ -363,13 +363,21 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
   relate<KDA>(sm.rows[0], sm.coef[0], warp, n0, lane);
   __syncthreads();
 
+  // A bf16 state under fp32 activations takes its tokens one by one, products and
+  // sum rounded each, as the definition writes them: the fp32 value that is then
+  // rounded to 16 bits depends on how tokens fall into groups and calls only
+  // through the sums' order. Grouped and fused, two to four times as many of the
+  // stored values came out a step apart from those of the plain rule, which the
+  // next call's fp32 outputs show (in single places by a thousandth of their
+  // size). Here that is worth its extra instructions and the later reads.
+  constexpr bool kStep = sizeof(T) == 4 && sizeof(ST) == 2;
   const bool ylane = warp >= kRecWarps / 2;             // this thread's part of the chain: Y or X
   const int c = tid % kRecCols;                         // of this column
   const bool c_ok = FULL || col0 + c < dv;
   for (int b = 0, slot3 = 0;; ++b) {
     const int p2 = p1 + n1, n2 = group_len(p2);      // 0 at the run's end
     const int slot1 = slot3 == 2 ? 0 : slot3 + 1, slot2 = slot3 == 0 ? 2 : slot3 - 1;
-    if (warp < n2)
+    if (!kStep && warp < n2)
       fetch<T, KDA>(A, t0 + int64_t(p2) + warp, h, hk, col0, lane, sm.rows[b & 1], sm.v[slot2], warp);
     const RecCoef<KDA> &C = sm.coef[b & 1];
     if (b) __syncthreads();           // the next group's rows have landed
@@ -444,7 +452,21 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
           o[(p0 + m) * o_stride + c] = from_f32<T>(y);
         }
     }
-    if (n1 > 0 || p1 == keep) {       // the state after this group is wanted
+    if (kStep && (n1 > 0 || p1 == keep)) {
+      const RecRows<KDA> &R = sm.rows[b & 1];
+#pragma unroll 1
+      for (int m = 0; m < n0; ++m) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(&sm.u[m][cl]);
+#pragma unroll
+        for (int i = 0; i < NP * 4; ++i) {
+          const int j = 32 * (i >> 2) + (i & 3) + g4;
+          const float k = R.k[m][j], a = R.a[m][KDA ? j : 0];
+          const Pair k2 = pair(k, k), a2 = pair(a, a);
+          S[i][0] = add2_apart(mul2(S[i][0], a2), mul2(w.x, k2));
+          S[i][1] = add2_apart(mul2(S[i][1], a2), mul2(w.y, k2));
+        }
+      }
+    } else if (n1 > 0 || p1 == keep) {   // the state after this group is wanted
       const Pair cl2 = KDA ? 0 : pair(C.c[n0 - 1], C.c[n0 - 1]);
 #pragma unroll
       for (int i = 0; i < NP * 4; ++i) {
@@ -486,6 +508,11 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
       }
     }
     if (n1 == 0) break;
+    if (kStep && n2 > 0) {            // this group's rows were read up to here
+      __syncthreads();
+      if (warp < n2)
+        fetch<T, KDA>(A, t0 + int64_t(p2) + warp, h, hk, col0, lane, sm.rows[b & 1], sm.v[slot2], warp);
+    }
     if (n2 > 0) land<T, KDA>(A, warp < n2, col0, lane, sm.rows[b & 1], sm.v[slot2], warp);
     p0 = p1; n0 = n1; p1 = p2; n1 = n2;
     slot3 = slot1;
@@ -680,7 +707,8 @@ __global__ void __launch_bounds__(32 * kOneWarps<ST, FULL>, 16 / kOneWarps<ST, F
     S[r].hide();
     Pair s[V / 2];
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) s[i] = fma2(u2[i], kk, mul2(aa, S[r].get(i)));
+    for (int i = 0; i < V / 2; ++i)   // products and sum rounded each: see kStep
+      s[i] = add2_apart(mul2(aa, S[r].get(i)), mul2(u2[i], kk));
     if (FULL || (col_ok && j < dk)) Piece<ST>::store(FULL ? st + r * step : dst, s);
     if (!FULL) {
       dst += step;

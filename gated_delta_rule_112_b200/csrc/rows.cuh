@@ -81,6 +81,13 @@ __device__ __forceinline__ Pair mul2(Pair a, Pair b) {
   return d;
 }
 
+// a + b with a rounding of its own: two single additions, since a paired
+// product and a paired addition come out as one fused operation.
+__device__ __forceinline__ Pair add2_apart(Pair a, Pair b) {
+  const float2 x = unpair(a), y = unpair(b);
+  return pair(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+}
+
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
