@@ -297,17 +297,19 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
 
   // The run. A bad one (tokens outside [0, T], keep outside its length, a slot
   // outside the pool, a slot that another run also names while one of the two
-  // writes it) is refused as a whole; a negative slot is padding.
+  // writes it) is refused as a whole; a negative slot is padding, whatever its
+  // boundaries say (a captured batch's unused runs may hold stale ones).
   const int slot = A.slots ? A.slots[n] : n;
   const int t0 = A.cu ? A.cu[n] : n * A.L, t1 = A.cu ? A.cu[n + 1] : t0 + A.L;
   const int kept = A.keep ? A.keep[n] : -2;
   const bool fresh = A.reset && A.reset[n];
+  if (slot < 0) return;
   if (t0 < 0 || t1 < t0 || t1 > A.T) {
     if (tid == 0 && A.status) atomicOr(A.status, kErrBadSeqlens);
     return;
   }
   const int len = t1 - t0;
-  if (slot < 0 || len == 0) return;
+  if (len == 0) return;
   const int keep = A.keep ? kept : len;
   bool bad = slot >= A.num_slots || keep < 0 || keep > len;
 

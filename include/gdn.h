@@ -409,7 +409,10 @@ int gdn_chunk_bwd_exact(const void *q, const void *k, const void *v, const float
  *              16-byte aligned. All arithmetic is fp32; a bf16 pool rounds the
  *              state once a call, when it is stored.
  *   slots      int32 [N] or NULL (run n uses slot n): where run n's state lies.
- *              Negative: run n is padding, nothing of it is read or written.
+ *              Negative: run n is padding, whatever its boundaries, keep and
+ *              reset are: no state is read or written for it and its outputs
+ *              are left alone. (With cu_seqlens NULL its tokens' rows exist
+ *              and may be read; what they hold is of no account.)
  *   cu_seqlens int32 [N + 1] or NULL: run n covers tokens [cu[n], cu[n+1])
  *              (empty runs allowed); tokens outside every run are left alone.
  *              NULL: T / N tokens a run, T a multiple of N.

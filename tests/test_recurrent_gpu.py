@@ -438,3 +438,20 @@ def test_workload_pool_step_full_size():
     for cu in (False, True):
         o, pool = call(d, cu=cu)
         check(d, o, pool)
+
+
+def test_padding_runs_may_have_any_boundaries():
+    """The unused runs at the end of a captured batch: negative slots with boundaries, keep points and
+    resets left over from an earlier batch. They are no error and change nothing."""
+    import gated_delta_rule_112_b200 as gdn
+    d = make([2, 3], 2, 2, 128, 128, BF, seed=36, spare=5)
+    ref, rpool = call(d)
+    slots = d["slots"].tolist()
+    status = gdn.status_block()
+    for tail in ([5, 3, 9], [0, 0, -7], [40, 2, 1 << 30]):
+        p = {**d, "cu": torch.tensor([0, 2, 5, *tail], dtype=torch.int32)}
+        out = torch.full(tuple(ref.shape), 7.0, dtype=BF, device="cuda")
+        o, pool = call(p, slots=[*slots, -1, -5, -1], keep=[2, 3, 9, -4, 1],
+                       reset=[False, False, True, True, False], out=out, status=status)
+        assert gdn.get_status(status) == gdn.OK
+        assert torch.equal(o, ref) and torch.equal(pool, rpool)
