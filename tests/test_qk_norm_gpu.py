@@ -475,3 +475,29 @@ def test_training_step_on_the_checkpoint(exact, bound):
     for i, n in enumerate(("dq", "dk")):
         dx, _ = grads_of(x[i], None, how, 1.0, torch.from_numpy(ref[n]).view(B * T, H, d))
         assert_close(n, np64(out[n]), dx.reshape(B, T, H, d), bound + tol(BF))
+
+
+def test_angles_are_as_near_at_every_position():
+    """Cosines and sines themselves, from rows of (1, 0) pairs, against angles reduced in rational
+    arithmetic. The part of a turn, doubled, is at most 1 and is rounded to fp32: 2^-25 half turns, so
+    pi 2^-25 rad. Sine and cosine of it are off by one unit in the last place of a value up to 1 at most:
+    2^-24. Products with 1 and 0 are exact."""
+    from fractions import Fraction
+    import gated_delta_rule_112_b200 as gdn
+    pi = Fraction(31415926535897932384626433832795028841971693993751058209749445923, 10 ** 64)
+    gen = torch.Generator().manual_seed(62)
+    f = torch.cat([inv_freq(64), torch.tensor([1.5, 37.0, 123.456, 1 / 3], dtype=torch.float64)])
+    rows = [torch.randint(lo, hi, (40,), generator=gen) for lo, hi in
+            ((0, 1 << 20), (1 << 27, 1 << 28), (1 << 30, (1 << 31) - 1), (-(1 << 31), -(1 << 30)))]
+    pos = torch.cat([*rows, torch.tensor([2 ** 31 - 1, -2 ** 31, 0])]).to(torch.int32)
+    x = torch.zeros(len(pos), 1, 2 * len(f))
+    x[..., 0::2] = 1
+    y, _ = gdn.qk_norm_rope_fwd(x.cuda(), None, norm="none", positions=pos.cuda(), inv_freq=f.cuda(),
+                                interleaved=True)
+    want = torch.empty(len(pos), 2 * len(f), dtype=torch.float64)
+    for t, p in enumerate(pos.tolist()):
+        for j, w in enumerate(f.tolist()):
+            a = p * Fraction(w)
+            a = float(a - 2 * pi * round(a / (2 * pi)))
+            want[t, 2 * j], want[t, 2 * j + 1] = math.cos(a), math.sin(a)
+    assert float((y[:, 0].cpu().double() - want).abs().max()) <= math.pi * 2.0 ** -25 + 2.0 ** -24
