@@ -944,7 +944,8 @@ int check_params(const gdn_qk_params *p) {
   if (p->T < 0 || p->H_q < 0 || p->H_k < 0 || p->d < 1 || p->rot < 0 || p->rot % 2 ||
       p->rot > p->d || p->norm < GDN_NORM_NONE || p->norm > GDN_NORM_RMS)
     return GDN_ERR_INVALID_ARG;
-  if (p->d > kMaxD) return GDN_ERR_UNSUPPORTED;
+  // a token's heads, and the step past the last of them, are counted in 32 bits
+  if (p->d > kMaxD || int64_t(p->H_q) + p->H_k > 1 << 30) return GDN_ERR_UNSUPPORTED;
   if (p->rot && p->T && (!p->positions || !p->inv_freq)) return GDN_ERR_INVALID_ARG;
   const size_t e = p->dtype == GDN_BF16 ? 2 : 4;
   if (!aligned(p->positions, 4) || !aligned(p->inv_freq, 8) || !aligned(p->w_q, e) ||

@@ -484,7 +484,8 @@ typedef struct {
 } gdn_packed;
 
 typedef struct {
-  int32_t T, H_q, H_k, d;          /* tokens; heads of q and of k (0: absent); d <= 256 */
+  int32_t T, H_q, H_k, d;          /* tokens; heads of q and of k (0: absent; 2^30
+                                    * together at most); d <= 256 */
   int32_t rot;                     /* elements of a head that turn: even, 0 .. d */
   int32_t interleaved;             /* which pairs turn together */
   int32_t norm;                    /* GDN_NORM_* */

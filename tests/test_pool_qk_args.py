@@ -159,3 +159,15 @@ def test_formula_gradients_against_differences(norm, interleaved):
             flat[i] = old
             num.view(-1)[i] = (vals[0] - vals[1]) / 2e-5
         assert float((num - grad).norm() / grad.norm()) < 1e-8
+
+
+def test_norm_refuses_more_heads_than_its_counters_hold(L):
+    k8 = ctypes.byref(gdn._PackedRows(1 << 20, 1 << 20))
+    for heads in (dict(H_q=2 ** 31 - 1, H_k=0), dict(H_q=2 ** 30, H_k=1), dict(H_q=2 ** 31 - 1, H_k=2 ** 31 - 1)):
+        p, r = ctypes.byref(params(T=1, d=1, rot=0, **heads)), ctypes.byref(rows(ts=1 << 40, hs=1))
+        assert L.gdn_qk_norm_rope_fwd(p, r, r, r, r, None, None, None) == gdn.ERR_UNSUPPORTED
+        assert L.gdn_qk_norm_rope_fwd_packed(p, k8, k8, r, r, None) == gdn.ERR_UNSUPPORTED
+        assert L.gdn_qk_norm_rope_bwd(p, r, r, gdn.F32, r, r, r, r, None, None, None, 0,
+                                      None) == gdn.ERR_UNSUPPORTED
+        assert L.gdn_qk_norm_rope_bwd_packed(p, r, r, gdn.F32, k8, k8, r, r, None, None, None, 0,
+                                             None) == gdn.ERR_UNSUPPORTED
