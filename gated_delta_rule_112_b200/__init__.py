@@ -410,7 +410,7 @@ def recurrent_fwd(q, k, v, g, beta, pool, slots=None, cu_seqlens=None, keep=None
             g.dtype == f32 and beta.dtype == f32 and
             k.shape == q.shape and v.shape[0] == T and out.shape == (T, Hv, dv) and
             g.shape == ((T, Hv, dk) if channel else (T, Hv)) and beta.shape == (T, Hv) and
-            pool.shape == (P, Hv, dk, dv) and
+            pool.shape == (P, Hv, dk, dv) and max(T, N, Hk, Hv, dk, dv) <= _INT32_MAX and
             (qe == 1 or dk == 1) and (ke == 1 or dk == 1) and (ve == 1 or dv == 1) and
             (qh == dk or Hk == 1) and (kh == dk or Hk == 1) and (vh == dv or Hv == 1) and
             g.is_contiguous() and beta.is_contiguous() and pool.is_contiguous() and
@@ -423,7 +423,7 @@ def recurrent_fwd(q, k, v, g, beta, pool, slots=None, cu_seqlens=None, keep=None
             f"{name}: q, k [T,H_k,d_k], v [T,H_v,d_v] and out of one type (bf16 or fp32), heads of a "
             "token next to each other; g [T,H_v] or [T,H_v,d_k] and beta [T,H_v] contiguous fp32; "
             "pool [num_slots,H_v,d_k,d_v] contiguous, bf16 or fp32; slots, keep [N] and cu_seqlens "
-            "[N+1] int32, reset [N] bool; status of 256 bytes; all on one CUDA device")
+            "[N+1] int32, reset [N] bool; status of 256 bytes; all on one CUDA device; sizes below 2^31")
     if T <= 1:                    # the stride of one token is of no account
         qs, ks, vs = max(qs, Hk * dk), max(ks, Hk * dk), max(vs, Hv * dv)
     rc = lib().gdn_recurrent_fwd(
@@ -436,6 +436,7 @@ def recurrent_fwd(q, k, v, g, beta, pool, slots=None, cu_seqlens=None, keep=None
 
 
 _DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
+_INT32_MAX = 2 ** 31 - 1          # ctypes would pass the low 32 bits of a larger size
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
@@ -535,6 +536,8 @@ def _qk_params(name, dev, qs, ks, dtype, w_q, w_k, positions, inv_freq, norm, ep
     """qs, ks: shapes of q and k (ks None without k)."""
     T, Hq, d = qs
     Hk = 0 if ks is None else ks[1]
+    if max(T, Hq, Hk, d) > _INT32_MAX:
+        raise ValueError(f"{name}: sizes of 2^31 and more")
     if not (dtype in _DTYPES and norm in _NORMS and (ks is None or (ks[0] == T and ks[2] == d)) and
             (positions is None) == (inv_freq is None) and (ks is not None or w_k is None)):
         raise ValueError(f"{name}: q and k [T,H,d] of bf16 or fp32, norm one of {sorted(_NORMS)}, "

@@ -171,3 +171,46 @@ def test_norm_refuses_more_heads_than_its_counters_hold(L):
                                       None) == gdn.ERR_UNSUPPORTED
         assert L.gdn_qk_norm_rope_bwd_packed(p, r, r, gdn.F32, k8, k8, r, r, None, None, None, 0,
                                              None) == gdn.ERR_UNSUPPORTED
+
+
+class Shaped:
+    """What the binding asks of a tensor, without its memory."""
+
+    def __init__(self, *shape, dtype=torch.bfloat16):
+        self.shape, self.dtype, self.nbytes = shape, dtype, 1 << 40
+
+    def stride(self):
+        out, s = [], 1
+        for n in reversed(self.shape):
+            out.append(s)
+            s *= n
+        return tuple(reversed(out))
+
+    def numel(self):
+        return self.stride()[0] * self.shape[0]
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+def test_binding_refuses_sizes_past_32_bits(L, monkeypatch):
+    """Sizes that ctypes would cut to their low 32 bits: 2^32 + 2 tokens would run as 2."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    f32, big = torch.float32, 2 ** 32 + 2
+    for T, N, Hk, Hv in ((big, 1, 1, 1), (big, big, 1, 1), (2, 1, big, big), (2 ** 31, 1, 1, 1)):
+        with pytest.raises(ValueError):
+            gdn.recurrent_fwd(Shaped(T, Hk, 8), Shaped(T, Hk, 8), Shaped(T, Hv, 8), Shaped(T, Hv, dtype=f32),
+                              Shaped(T, Hv, dtype=f32), Shaped(N, Hv, 8, 8, dtype=f32), out=Shaped(T, Hv, 8))
+    how = (torch.bfloat16, None, None, None, None, "l2", 1e-6, False, 0.0, 1.0, 1.0)
+    for qs, ks in (((big, 1, 8), None), ((2, big, 8), None), ((2, 1, big), None), ((2, 1, 8), (2, big, 8))):
+        with pytest.raises(ValueError):
+            gdn._qk_params("norm", 0, qs, ks, *how)
