@@ -418,12 +418,12 @@ def recurrent_fwd(q, k, v, g, beta, pool, slots=None, cu_seqlens=None, keep=None
             _same_device(dev, k, v, g, beta, pool, slots, cu_seqlens, keep, reset, out, status) and
             _index(slots, torch.int32, N) and _index(cu_seqlens, torch.int32, N + 1) and
             _index(keep, torch.int32, N) and _index(reset, torch.bool, N) and
-            (status is None or status.nbytes >= 256)):
+            (status is None or status.nbytes >= 256 and status.is_contiguous())):
         raise ValueError(
             f"{name}: q, k [T,H_k,d_k], v [T,H_v,d_v] and out of one type (bf16 or fp32), heads of a "
             "token next to each other; g [T,H_v] or [T,H_v,d_k] and beta [T,H_v] contiguous fp32; "
             "pool [num_slots,H_v,d_k,d_v] contiguous, bf16 or fp32; slots, keep [N] and cu_seqlens "
-            "[N+1] int32, reset [N] bool; status of 256 bytes; all on one CUDA device; sizes below 2^31")
+            "[N+1] int32, reset [N] bool; status of 256 bytes in a row; all on one CUDA device; sizes below 2^31")
     if T <= 1:                    # the stride of one token is of no account
         qs, ks, vs = max(qs, Hk * dk), max(ks, Hk * dk), max(vs, Hv * dv)
     rc = lib().gdn_recurrent_fwd(
@@ -471,6 +471,16 @@ def _same_device(dev, *ts):
         if t is not None and t.get_device() != dev:
             return False
     return dev >= 0
+
+
+def _scratch(name, t, need, dev):
+    """Whether the caller's workspace is to be used: it may be too small or None,
+    but what is written to must be one piece of this device's memory."""
+    if t is None or t.nbytes < need:
+        return False
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: workspace not contiguous or on another device")
+    return True
 
 
 def _index(t, dtype, n):
@@ -656,10 +666,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, w_q=None, w_k=None, positions=None, i
     need = 0
     if dwq is not None or dwk is not None:
         need = lib().gdn_qk_norm_rope_bwd_workspace_size(p)
-        if workspace is None or workspace.nbytes < need:
+        if not _scratch(name, workspace, need, dev):
             workspace = dq_out.new_empty(need, dtype=torch.uint8)
-        elif workspace.get_device() != dev:
-            raise ValueError(f"{name}: workspace on another device")
     s = _raw_stream(dev)
     if packed:
         rc = lib().gdn_qk_norm_rope_bwd_packed(
@@ -732,6 +740,7 @@ def chunk_bwd_packed(ckpt: Checkpoint, g, beta, d_o, initial_state=None, cu_seql
             return chunk_bwd_packed(ckpt, g, beta, d_o, initial_state, cu_seqlens, d_final_state,
                                     workspace, exact=exact, **norm)
     B, T, H, dk, dv = ckpt.shape
+    _scratch("chunk_bwd_packed", workspace, 0, dev)
     qn, kn = qk_norm_rope_fwd(ckpt.q, ckpt.k, dtype=ckpt.dtype, **norm)
     v = unpack(ckpt.v, ckpt.dtype)
     out = chunk_bwd(qn.view(B, T, H, dk), kn.view(B, T, H, dk), v.view(B, T, H, dv), g, beta, d_o,

@@ -214,3 +214,47 @@ def test_binding_refuses_sizes_past_32_bits(L, monkeypatch):
     for qs, ks in (((big, 1, 8), None), ((2, big, 8), None), ((2, 1, big), None), ((2, 1, 8), (2, big, 8))):
         with pytest.raises(ValueError):
             gdn._qk_params("norm", 0, qs, ks, *how)
+
+
+class Strided(Shaped):
+    """Fewer bytes of memory than its elements would take, as an expanded tensor's."""
+
+    def is_contiguous(self):
+        return False
+
+
+def test_binding_refuses_memory_in_pieces_to_write_to(L, monkeypatch):
+    """An expanded workspace or status block counts more bytes than it has."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    f32 = torch.float32
+    with pytest.raises(ValueError):
+        gdn.recurrent_fwd(Shaped(2, 1, 8), Shaped(2, 1, 8), Shaped(2, 1, 8), Shaped(2, 1, dtype=f32),
+                          Shaped(2, 1, dtype=f32), Shaped(2, 1, 8, 8, dtype=f32), out=Shaped(2, 1, 8),
+                          status=Strided(256, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        gdn._scratch("norm", Strided(1 << 20, dtype=torch.uint8), 1 << 20, 0)
+    with pytest.raises(ValueError):
+        gdn._scratch("norm", Shaped(1 << 20, dtype=torch.uint8), 1 << 20, 1)
+    assert gdn._scratch("norm", Shaped(1 << 20, dtype=torch.uint8), 1 << 20, 0)
+    assert not gdn._scratch("norm", None, 1 << 20, 0)
+    codes, scales = Shaped(6, 2, 128, dtype=torch.float8_e4m3fn), Shaped(6, 2, 4, dtype=torch.uint8)
+    ckpt = gdn.Checkpoint(*[gdn.Packed(codes, scales)] * 3, (1, 6, 2, 128, 128), torch.bfloat16)
+    with pytest.raises(ValueError):
+        gdn.chunk_bwd_packed(ckpt, None, None, None, workspace=Strided(1 << 30, dtype=torch.uint8))
+
+
+@pytest.mark.gpu
+def test_workspaces_on_the_gpu(L):
+    """What the binding takes and refuses as a workspace, with real tensors."""
+    gen = torch.Generator().manual_seed(1)
+    q, k, dy = (torch.randn(5, 2, 64, generator=gen).to(torch.bfloat16).cuda() for _ in range(3))
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    ref = gdn.qk_norm_rope_bwd(dy, dy, q, k, w_q=w, w_k=w)
+    need = 1 << 20
+    ok = gdn.qk_norm_rope_bwd(dy, dy, q, k, w_q=w, w_k=w,
+                              workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    assert all(torch.equal(ref[n], ok[n]) for n in ref)
+    one = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError):
+        gdn.qk_norm_rope_bwd(dy, dy, q, k, w_q=w, w_k=w, workspace=one.expand(need))
+    assert int(one) == 0
