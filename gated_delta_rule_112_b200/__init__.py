@@ -705,6 +705,28 @@ class Checkpoint(NamedTuple):
     dtype: torch.dtype
 
 
+def _step_args(name, dev, shape, dtype, g, beta, initial_state, cu_seqlens, d_final_state=None,
+               **rows):
+    """Refuses what the chunked passes would read as something else, or past its end.
+    shape: (B, T, H, d_k, d_v); rows: tensors of the step by name."""
+    B, T, H, dk, dv = shape
+    N = B if cu_seqlens is None else cu_seqlens.numel() - 1
+
+    def fits(t, want, want_dtype):
+        return t is None or (t.shape == want and t.dtype == want_dtype and t.get_device() == dev)
+
+    for what, t in rows.items():
+        if not fits(t, (B, T, H, dk if what in "qk" else dv), dtype):
+            raise ValueError(f"{name}: {what} has shape {tuple(t.shape)} and {t.dtype}")
+    f32 = torch.float32
+    if g is None or beta is None or not (
+            fits(g, (B, T, H), f32) and fits(beta, (B, T, H), f32) and
+            fits(initial_state, (N, H, dk, dv), f32) and fits(d_final_state, (N, H, dk, dv), f32) and
+            fits(cu_seqlens, (N + 1,), torch.int32)):
+        raise ValueError(f"{name}: g and beta [B,T,H], states [N,H,d_k,d_v] (fp32) and cu_seqlens [N+1] "
+                         "(int32) on the rows' device")
+
+
 def chunk_fwd_packed(q, k, v, g, beta, initial_state=None, cu_seqlens=None, chunk=64,
                      output_final_state=True, stream=None, **norm):
     """``qk_norm_rope_fwd`` (its keywords in ``norm``; positions [B*T]) and
@@ -719,6 +741,8 @@ def chunk_fwd_packed(q, k, v, g, beta, initial_state=None, cu_seqlens=None, chun
                                     output_final_state, **norm)
     B, T, H, dk = q.shape
     dv = v.shape[-1]
+    _step_args("chunk_fwd_packed", dev, (B, T, H, dk, dv), q.dtype, g, beta, initial_state, cu_seqlens,
+               q=q, k=k, v=v)
     flat = [x.reshape(B * T, H, x.shape[-1]) for x in (q, k, v)]
     qn, kn, q8, k8 = qk_norm_rope_fwd(flat[0], flat[1], pack=True, **norm)
     v8 = pack(flat[2])
@@ -741,6 +765,8 @@ def chunk_bwd_packed(ckpt: Checkpoint, g, beta, d_o, initial_state=None, cu_seql
                                     workspace, exact=exact, **norm)
     B, T, H, dk, dv = ckpt.shape
     _scratch("chunk_bwd_packed", workspace, 0, dev)
+    _step_args("chunk_bwd_packed", dev, ckpt.shape, ckpt.dtype, g, beta, initial_state, cu_seqlens,
+               d_final_state, d_o=d_o)
     qn, kn = qk_norm_rope_fwd(ckpt.q, ckpt.k, dtype=ckpt.dtype, **norm)
     v = unpack(ckpt.v, ckpt.dtype)
     out = chunk_bwd(qn.view(B, T, H, dk), kn.view(B, T, H, dk), v.view(B, T, H, dv), g, beta, d_o,

@@ -258,3 +258,30 @@ def test_workspaces_on_the_gpu(L):
     with pytest.raises(ValueError):
         gdn.qk_norm_rope_bwd(dy, dy, q, k, w_q=w, w_k=w, workspace=one.expand(need))
     assert int(one) == 0
+
+
+STEP_BAD = [dict(v=(2, 3, 2, 128, "f32")), dict(k=(2, 3, 4, 64, "bf16")), dict(k=(3, 2, 2, 128, "bf16")),
+            dict(beta=(2, 3, 2, "bf16")), dict(beta=(2, 3, 1, "f32")), dict(g=(2, 3, 2, "bf16")), dict(g=None),
+            dict(initial_state=(1, 2, 128, 128, "f32")), dict(initial_state=(2, 2, 128, 128, "bf16")),
+            dict(cu_seqlens=(3, "i64")), dict(d_o=(2, 3, 2, 64, "bf16")), dict(d_o=(2, 3, 2, 128, "f32")),
+            dict(d_final_state=(2, 1, 128, 128, "f32"))]
+
+
+@pytest.mark.parametrize("bad", STEP_BAD)
+def test_training_step_refuses_what_it_would_misread(L, monkeypatch, bad):
+    """Tensors of another type or fewer elements than the chunked passes would read."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    types = dict(f32=torch.float32, bf16=torch.bfloat16, i64=torch.int64)
+    a = dict(q=(2, 3, 2, 128, "bf16"), k=(2, 3, 2, 128, "bf16"), v=(2, 3, 2, 128, "bf16"), g=(2, 3, 2, "f32"),
+             beta=(2, 3, 2, "f32"), d_o=(2, 3, 2, 128, "bf16"))
+    a = {n: s and Shaped(*s[:-1], dtype=types[s[-1]]) for n, s in {**a, **bad}.items()}
+    d_o, more = a.pop("d_o"), {n: a.pop(n) for n in list(a) if n in ("initial_state", "cu_seqlens")}
+    last = {n: a.pop(n) for n in list(a) if n == "d_final_state"}
+    if not ({"d_o", "d_final_state"} & bad.keys()):
+        with pytest.raises(ValueError):
+            gdn.chunk_fwd_packed(**a, **more)
+    if not ({"q", "k", "v"} & bad.keys()):
+        p = gdn.Packed(Shaped(6, 2, 128, dtype=torch.float8_e4m3fn), Shaped(6, 2, 4, dtype=torch.uint8))
+        ckpt = gdn.Checkpoint(p, p, p, (2, 3, 2, 128, 128), torch.bfloat16)
+        with pytest.raises(ValueError):
+            gdn.chunk_bwd_packed(ckpt, a["g"], a["beta"], d_o, **more, **last)
