@@ -58,7 +58,7 @@ struct RecArgs {
   void *o;
   uint32_t *status;
   int64_t q_stride, k_stride, v_stride, num_slots;
-  int N, T, L, Hk, Hv, dk, dv;      // L: tokens per run without cu
+  int N, T, L, Hv, dk, dv;          // L: tokens per run without cu
   int splits;                       // CTAs per state: 1 or 2
   float per_k;                      // H_k / H_v
   bool vec;                         // q, k, v rows can be read four elements at a time
@@ -108,17 +108,14 @@ __device__ __forceinline__ int key_head(const RecArgs &A, int h) {
   return int((float(h) + 0.5f) * A.per_k);
 }
 
+// Up to four elements, one by one; zero past the n-th.
 template <typename T>
-__device__ __forceinline__ float4 load4(const T *p, int n, bool vec) {
+__device__ __forceinline__ float4 load4(const T *p, int n) {
   float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (vec) {
-    if (n > 0) r = ld4(p);
-  } else {
-    if (n > 0) r.x = to_f32(p[0]);
-    if (n > 1) r.y = to_f32(p[1]);
-    if (n > 2) r.z = to_f32(p[2]);
-    if (n > 3) r.w = to_f32(p[3]);
-  }
+  if (n > 0) r.x = to_f32(p[0]);
+  if (n > 1) r.y = to_f32(p[1]);
+  if (n > 2) r.z = to_f32(p[2]);
+  if (n > 3) r.w = to_f32(p[3]);
   return r;
 }
 
@@ -156,10 +153,10 @@ __device__ __forceinline__ void fetch(const RecArgs &A, int64_t t, int h, int hk
     }
     if (c < kRecCols && col0 + c < A.dv) copy_async(reinterpret_cast<T *>(v[m]) + c, vp, 4 * sizeof(T));
   } else {
-    sts4(&R.k[m][c], load4(kp, A.dk - c, false));
-    sts4(&R.q[m][c], load4(qp, A.dk - c, false));
-    if (KDA) sts4(&R.a[m][c], load4(gp + c, A.dk - c, false));
-    if (c < kRecCols) sts4(&v[m][c], load4(vp, A.dv - col0 - c, false));
+    sts4(&R.k[m][c], load4(kp, A.dk - c));
+    sts4(&R.q[m][c], load4(qp, A.dk - c));
+    if (KDA) sts4(&R.a[m][c], load4(gp + c, A.dk - c));
+    if (c < kRecCols) sts4(&v[m][c], load4(vp, A.dv - col0 - c));
   }
   if (lane == 0) {
     if (!KDA) copy_async(&R.a[m][0], gp, 4);
@@ -794,7 +791,7 @@ extern "C" int gdn_recurrent_fwd(const void *q, const void *k, const void *v, co
   A.num_slots = num_slots;
   A.N = N; A.T = T; A.L = cu_seqlens ? 0 : T / N;
   A.per_k = float(H_k) / float(H_v);
-  A.Hk = H_k; A.Hv = H_v; A.dk = d_k; A.dv = d_v;
+  A.Hv = H_v; A.dk = d_k; A.dv = d_v;
   A.vec = d_k % 4 == 0 && q_stride % 4 == 0 && k_stride % 4 == 0 && v_stride % 4 == 0 &&
           aligned(q, 4 * e) && aligned(k, 4 * e) && aligned(v, 4 * e) && (!channel_gate || aligned(g, 16));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
