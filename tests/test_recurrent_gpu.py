@@ -455,3 +455,84 @@ def test_padding_runs_may_have_any_boundaries():
                        reset=[False, False, True, True, False], out=out, status=status)
         assert gdn.get_status(status) == gdn.OK
         assert torch.equal(o, ref) and torch.equal(pool, rpool)
+
+
+# fp32 rows on a bf16 pool: the kernel for runs takes the tokens' updates one by one and fetches later.
+STEP = [
+    # lens, Hk, Hv, dk, dv, channel gate; runs of three groups of four and more
+    ([9, 30, 13], 2, 4, 128, 128, False),
+    ([9, 30, 13], 2, 4, 128, 128, True),
+    ([17, 0, 12, 21], 1, 2, 33, 12, False),            # rows that are not copied in pieces
+    ([17, 0, 12, 21], 1, 2, 33, 12, True),
+    ([64, 10], 3, 3, 96, 80, False),
+    ([25], 1, 4, 64, 128, True),
+]
+
+
+@pytest.mark.parametrize("part", [False, True])
+@pytest.mark.parametrize("case", range(len(STEP)))
+def test_fp32_rows_on_a_bf16_pool(case, part):
+    lens, Hk, Hv, dk, dv, channel = STEP[case]
+    d = make(lens, Hk, Hv, dk, dv, F, BF, channel, seed=200 + case, beta_scale=2.0)
+    how = {}
+    if part:                                           # keep points inside groups, fresh states
+        how = dict(keep=[[6, 5, 0, n][i] if n else 0 for i, n in enumerate(lens)],
+                   reset=[i % 2 == 1 for i in range(len(lens))])
+    o, pool = call(d, **how)
+    check(d, o, pool, **how)
+
+
+def rounded_update():
+    """Twelve tokens on a state of ones: k of token t is (x, -x) in rows 2t and 2t + 1, so S k is zero in any
+    order, k_l . k_m is zero and u is v. The rule then stores 1 + v x and 1 - v x, with a rounding of the
+    product and one of the sum. Three quarters of the columns hold a v for which one fused rounding of 1 + v x
+    ends on the other side of a bf16 border. Returns k, v, the stored state and the fused one."""
+    rng = np.random.default_rng(5)
+    k, v = np.zeros((12, 128), np.float32), rng.standard_normal((12, 128)).astype(np.float32)
+    at = np.float32(2.0 ** -8 + 2.0 ** -24)            # 1 + this is halfway between two fp32 numbers
+    for t in range(12):
+        found = []
+        while not found:
+            x = np.float32(rng.uniform(0.4, 0.7))
+            w = (np.float64(at) / np.float64(x)).astype(np.float32)
+            for u in (np.nextafter(w, np.float32(0)), w, np.nextafter(w, np.float32(1))):
+                if u * x == at and np.float64(u) * np.float64(x) > np.float64(at):
+                    found.append(u)
+        k[t, 2 * t], k[t, 2 * t + 1] = x, -x
+        v[t, :96] = np.resize(np.array(found, np.float32), 96)
+    one, both = np.float32(1), k.T[:, :, None] * v[None]            # [row, token, column], rounded
+    step, fused = np.ones((128, 128), np.float32), np.ones((128, 128), np.float32)
+    for j in range(24):
+        step[j] = one + both[j, j // 2]
+        fused[j] = (1 + np.float64(k[j // 2, j]) * np.float64(v[j // 2])).astype(np.float32)
+    to = lambda x: torch.from_numpy(x).to(BF)  # noqa: E731
+    return torch.from_numpy(k), torch.from_numpy(v), to(step), to(fused)
+
+
+@pytest.mark.parametrize("channel", [False, True])
+@pytest.mark.parametrize("one", [False, True])
+def test_fp32_rows_on_a_bf16_pool_round_products_and_sums(one, channel):
+    """The stored state of a run, and of single tokens, is the rule's own, bit for bit."""
+    import gated_delta_rule_112_b200 as gdn
+    k, v, step, fused = rounded_update()
+    assert int((step != fused).sum()) >= 12 * 96
+    n = 12 if one else 1
+    pool = torch.ones(n, 1, 128, 128, dtype=BF, device="cuda")
+    k, v = k[:, None].cuda(), v[:, None].cuda()
+    g = torch.zeros(12, 1, 128, device="cuda") if channel else torch.zeros(12, 1, device="cuda")
+    gdn.recurrent_fwd(k, k, v, g, torch.ones(12, 1, device="cuda"), pool, slots=ints(list(range(n))))
+    if one:                                            # each token changed its own two rows of its own state
+        rows = torch.arange(24)
+        assert torch.equal(pool[rows // 2, 0, rows].cpu(), step[:24])
+    else:
+        assert torch.equal(pool[0, 0].cpu(), step)
+
+
+def test_calls_repeat_bit_for_bit():
+    """One token of one sequence, a batch of them and runs: the same inputs give the same bits."""
+    for lens, Hk, Hv, dtype, pdt, cu in (([1], 16, 16, BF, F, False), ([1] * 64, 8, 16, BF, BF, False),
+                                         ([3, 17, 1, 6], 2, 4, F, F, True), ([9, 14], 2, 2, F, BF, True)):
+        d = make(lens, Hk, Hv, 128, 128, dtype, pdt, seed=210)
+        first = call(d, cu=cu)
+        for _ in range(3):
+            assert all(torch.equal(a, b) for a, b in zip(call(d, cu=cu), first))
