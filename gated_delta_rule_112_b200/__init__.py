@@ -688,7 +688,8 @@ def pack(x, stream=None) -> Packed:
 
 
 def unpack(x: Packed, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
-    """The rows that 8-bit rows stand for (exact in bf16 and fp32)."""
+    """The rows that 8-bit rows stand for: exact in fp32, and in bf16 but for fp32
+    rows below 2^-115 or so, whose codes reach under bf16's smallest number."""
     return qk_norm_rope_fwd(x, None, norm="none", dtype=dtype, stream=stream)[0]
 
 

@@ -41,7 +41,7 @@
 // smallest (e >= -127) with max|x| <= 448 * 2^e over the block's finite
 // elements, and are stored as e4m3 of x 2^-e (to nearest even); an element that
 // is not finite becomes NaN. One byte e + 127 a block: no code is rounded twice
-// and 2^e times a code is exact in bf16.
+// and 2^e times a code is exact in bf16 (for e >= -124, or rows that were bf16).
 #include <cuda_fp8.h>
 
 #include "gdn_internal.cuh"

@@ -477,8 +477,11 @@ typedef struct {
  * contiguous. Element e stands for codes[e] * 2^(scales[e / 32] - 127). The
  * scale is the smallest power of two (down to 2^-127) that takes the block's
  * largest finite magnitude to 448 or less; codes are rounded to nearest even;
- * what is not finite becomes NaN. Exact in bf16 and fp32, but that magnitudes
- * from 1.9375 * 2^127 up are rounded to 2^128, an infinity there. */
+ * what is not finite becomes NaN. What the rows stand for is exact in fp32, and
+ * in bf16 too, with two exceptions: magnitudes from 1.9375 * 2^127 up are rounded
+ * to 2^128, an infinity in either type; and fp32 rows whose scale is below 2^-124
+ * may stand for multiples of as little as 2^-136, which bf16 (2^-133 and up) rounds
+ * to nearest even. */
 typedef struct {
   uint8_t *codes, *scales;
 } gdn_packed;

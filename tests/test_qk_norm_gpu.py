@@ -501,3 +501,23 @@ def test_angles_are_as_near_at_every_position():
             a = float(a - 2 * pi * round(a / (2 * pi)))
             want[t, 2 * j], want[t, 2 * j + 1] = math.cos(a), math.sin(a)
     assert float((y[:, 0].cpu().double() - want).abs().max()) <= math.pi * 2.0 ** -25 + 2.0 ** -24
+
+
+def test_smallest_rows_between_the_types():
+    """fp32 rows below bf16's range: their codes stand for multiples of 2^-136, exact in fp32 and rounded to
+    nearest even in bf16. bf16 rows of that size come back exactly in either type."""
+    import gated_delta_rule_112_b200 as gdn
+    gen = torch.Generator().manual_seed(63)
+    x = torch.randn(64, 3, 96, generator=gen) * torch.exp2(-torch.arange(64.0) / 2 - 110)[:, None, None]
+    inexact = 0
+    for dtype in (F, BF):
+        rows = x.to(dtype)
+        p = gdn.pack(rows.cuda())
+        codes, scales = plain_pack(rows)
+        assert torch.equal(p.scales.cpu(), scales) and torch.equal(p.codes.cpu().double(), codes)
+        stands = value(p)
+        assert torch.equal(gdn.unpack(p, F).cpu().double(), stands)
+        back = gdn.unpack(p).cpu()
+        assert torch.equal(back, stands.float().to(BF))       # stands.float() is exact: one rounding
+        inexact = int((back.double() != stands).sum())
+        assert (inexact > 0) == (dtype == F)
