@@ -521,3 +521,36 @@ def test_smallest_rows_between_the_types():
         assert torch.equal(back, stands.float().to(BF))       # stands.float() is exact: one rounding
         inexact = int((back.double() != stands).sum())
         assert (inexact > 0) == (dtype == F)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("norm", ["l2", "rms", "none"])
+def test_gradients_of_heads_of_one_element(norm, dtype, packed):
+    """dx = r dh (1 - h^2), which cancels as eps goes to zero, so each element against r dh. Errors in units of
+    2^-24: r 5 (a sum and two products halved, and two units in the last place of the reciprocal root), which
+    h^2 has twice; the products x r, x dh and their product 3; w + offset, its product, the last difference and
+    product 4: 17, taken as 20. Stored in bf16, half a step of the value more."""
+    import gated_delta_rule_112_b200 as gdn
+    gen = torch.Generator().manual_seed(64)
+    for eps, weights in ((1e-6, False), (1e-6, True), (0.5, True), (0.5, False)):
+        q, k = ((2 * torch.randn(h * 7, generator=gen)).to(dtype).view(7, h, 1) for h in (3, 2))
+        w = [(1 + 0.3 * torch.randn(1, generator=gen)).to(dtype) if weights else None for _ in "qk"]
+        dy = [torch.randn(x.shape, generator=gen) for x in (q, k)]
+        how = dict(norm=norm, eps=eps, weight_offset=0.25)
+        src = [gdn.pack(x.cuda()) for x in (q, k)] if packed else [q.cuda(), k.cuda()]
+        more = dict(dtype=dtype) if packed else {}
+        out = gdn.qk_norm_rope_bwd(dy[0].cuda(), dy[1].cuda(), *src, **more, **dev(how, w))
+        for i, (x, n) in enumerate(((q, "q"), (k, "k"))):
+            x = (value(src[i]) if packed else x).double()
+            ref, dw = grads_of(x, w[i], how, 1.0, dy[i])
+            r = (x * x + eps).rsqrt() if norm != "none" else torch.ones_like(x)
+            dh = dy[i].double() * (w[i].double() + 0.25 if weights else 1.0)
+            ref = torch.from_numpy(ref)
+            bound = 20 * 2.0 ** -24 * (r * dh).abs()
+            if dtype == BF:
+                bound = bound * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs()
+            off = (out["d" + n].cpu().double() - ref).abs()
+            assert bool((off <= bound).all()), float((off / bound).max())
+            if weights:
+                assert_close("dw_" + n, np64(out["dw_" + n]), dw, TOL_F32)
