@@ -554,3 +554,59 @@ def test_gradients_of_heads_of_one_element(norm, dtype, packed):
             assert bool((off <= bound).all()), float((off / bound).max())
             if weights:
                 assert_close("dw_" + n, np64(out["dw_" + n]), dw, TOL_F32)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "bf16_exact", "f32", "short"])
+def test_training_step_with_states_weights_and_boundaries(kind):
+    """chunk_fwd_packed and chunk_bwd_packed with all that they take: packed sequences (one of them empty) or
+    equal ones, initial states, gradients of the final ones, weighted norms, part of the head turned.
+
+    The chunked pass's gradients are held to its own bound b. The norm takes dq through a map whose norm is at
+    most q_scale rope_scale max(r |w + offset|), so what b leaves in dq becomes at most that times |dq|; dw sums
+    dz h over rows, at most b |dz| times the longest column of h (Cauchy-Schwarz). Roundings of the norm's own
+    come on top: tol of the stored type."""
+    import gated_delta_rule_112_b200 as gdn
+    dtype, d, dv, exact, b = dict(bf16=(BF, 128, 128, False, TOL_BF16), bf16_exact=(BF, 128, 128, True, TOL_F32),
+                                  f32=(F, 64, 48, False, TOL_F32), short=(BF, 128, 128, False, TOL_BF16))[kind]
+    lens = [1, 1] if kind == "short" else [70, 0, 61]
+    cu = None if kind == "short" else torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32)
+    B, T, H, N = (2, 1, 3, 2) if kind == "short" else (1, sum(lens), 2, 3)
+    gen = torch.Generator().manual_seed(91)
+    q, k = (torch.randn(B, T, H, d, generator=gen).to(dtype) for _ in "qk")
+    v, d_o = (torch.randn(B, T, H, dv, generator=gen).to(dtype) for _ in "vo")
+    g = -torch.nn.functional.softplus(torch.randn(B, T, H, generator=gen) - 2)
+    beta = torch.sigmoid(torch.randn(B, T, H, generator=gen))
+    s0, ds = (0.3 * torch.randn(N, H, d, dv, generator=gen) for _ in "ab")
+    w = [(0.9 + 0.1 * torch.rand(d, generator=gen)).to(dtype) for _ in "qk"]
+    how = dict(norm="rms", positions=torch.arange(B * T, dtype=torch.int32) + 77, inv_freq=inv_freq(32),
+               weight_offset=float(np.float32(d ** -0.5 - 0.95)),      # keys of about unit length, as the rule wants
+               rope_scale=1.1, eps=1e-5)
+    scale = [0.5, 1.0]
+    kw = dict(dev(how, w), q_scale=scale[0])
+    flat = [x.view(B * T, H, d) for x in (q, k)]
+    o, fs, ck = gdn.chunk_fwd_packed(*(x.cuda() for x in (q, k, v, g, beta)), s0.cuda(),
+                                     None if cu is None else cu.cuda(), **kw)
+    rows = [plain(x, y, how, s).to(dtype).view(B, T, H, d) for x, y, s in zip(flat, w, scale)]
+    npcu = None if cu is None else cu.numpy()
+    ro, rfs = oracle.chunk_fwd(np64(rows[0]), np64(rows[1]), np64(v), np64(g), np64(beta), np64(s0), npcu)
+    fwd = TOL_BF16 if dtype == BF else TOL_F32
+    assert_close("o", np64(o), ro, fwd)
+    assert_close("final_state", np64(fs), rfs, fwd)
+    out = gdn.chunk_bwd_packed(ck, g.cuda(), beta.cuda(), d_o.cuda(), s0.cuda(),
+                               None if cu is None else cu.cuda(), ds.cuda(), exact=exact, **kw)
+    x = [value(y) for y in ck[:3]]
+    sq, sk = (np64(y.view(B, T, H, d)) for y in gdn.qk_norm_rope_fwd(ck.q, ck.k, dtype=dtype, **kw))
+    ref = oracle.chunk_bwd(sq, sk, x[2].view(B, T, H, dv).numpy(), np64(g), np64(beta), np64(d_o), np64(s0), npcu,
+                           np64(ds))
+    for n in ("dv", "dg", "dbeta", "d_initial_state"):
+        assert_close(n, np64(out[n]), ref[n], b)
+    for i, n in enumerate(("dq", "dk")):
+        dy = torch.from_numpy(ref[n]).view(B * T, H, d)
+        dx, dw = grads_of(x[i], w[i], how, scale[i], dy)
+        r = (x[i].detach().square().mean(-1, keepdim=True) + how["eps"]).rsqrt()
+        weight, h = w[i].double() + how["weight_offset"], x[i].detach() * r
+        dz = scale[i] * how["rope_scale"] * float(dy.norm())
+        off = np.linalg.norm(np64(out[n]).reshape(dx.shape) - dx)
+        assert off <= b * float((r * weight.abs()).max()) * dz + tol(dtype) * np.linalg.norm(dx), (n, off)
+        off = np.linalg.norm(np64(out["dw_" + n[1]]) - dw)
+        assert off <= (b + TOL_F32) * dz * float(h.square().sum((0, 1)).max().sqrt()), (n, off)
