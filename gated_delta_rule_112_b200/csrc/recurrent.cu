@@ -300,13 +300,12 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
   const int t0 = A.cu ? A.cu[n] : n * A.L, t1 = A.cu ? A.cu[n + 1] : t0 + A.L;
   const int kept = A.keep ? A.keep[n] : -2;
   const bool fresh = A.reset && A.reset[n];
-  if (slot < 0) return;
-  if (t0 < 0 || t1 < t0 || t1 > A.T) {
-    if (tid == 0 && A.status) atomicOr(A.status, kErrBadSeqlens);
+  const bool outside = t0 < 0 || t1 < t0 || t1 > A.T;
+  const int len = t1 - t0;
+  if (outside || slot < 0 || len == 0) {
+    if (outside && slot >= 0 && tid == 0 && A.status) atomicOr(A.status, kErrBadSeqlens);
     return;
   }
-  const int len = t1 - t0;
-  if (len == 0) return;
   const int keep = A.keep ? kept : len;
   bool bad = slot >= A.num_slots || keep < 0 || keep > len;
 
