@@ -108,6 +108,24 @@ __device__ __forceinline__ int key_head(const RecArgs &A, int h) {
   return int((float(h) + 0.5f) * A.per_k);
 }
 
+// Bounds checks (GDN_CHECKS builds): n elements from p on, of a buffer of extent
+// elements; what lies outside is skipped and recorded in the status block.
+#define REC_IN_BOUNDS(base, p, n, extent) \
+  GDN_IN_BOUNDS(A.status, (p) - (base), static_cast<long long>(extent) - (n) + 1)
+#if GDN_CHECKS
+__device__ __forceinline__ int64_t key_extent(const RecArgs &A, int64_t stride) {
+  return int64_t(A.T - 1) * stride + int64_t(key_head(A, A.Hv - 1) + 1) * A.dk;
+}
+__device__ __forceinline__ int64_t value_extent(const RecArgs &A) {
+  return int64_t(A.T - 1) * A.v_stride + int64_t(A.Hv) * A.dv;
+}
+__device__ __forceinline__ int64_t gate_extent(const RecArgs &A, bool kda) {
+  return int64_t(A.T) * A.Hv * (kda ? A.dk : 1);
+}
+__device__ __forceinline__ int64_t pool_extent(const RecArgs &A) { return A.num_slots * A.Hv * A.dk * A.dv; }
+__device__ __forceinline__ int64_t out_extent(const RecArgs &A) { return int64_t(A.T) * A.Hv * A.dv; }
+#endif
+
 // Up to four elements, one by one; zero past the n-th.
 template <typename T>
 __device__ __forceinline__ float4 load4(const T *p, int n) {
@@ -145,6 +163,15 @@ __device__ __forceinline__ void fetch(const RecArgs &A, int64_t t, int h, int hk
   const T *qp = static_cast<const T *>(A.q) + t * A.q_stride + int64_t(hk) * A.dk + c;
   const T *vp = static_cast<const T *>(A.v) + t * A.v_stride + int64_t(h) * A.dv + col0 + c;
   const float *gp = A.g + (t * A.Hv + h) * (KDA ? A.dk : 1);
+  const int kn = min(4, A.dk - c), vn = min(4, A.dv - col0 - c);      // what there is of the lane's four
+  if (kn > 0 && !(REC_IN_BOUNDS(static_cast<const T *>(A.k), kp, kn, key_extent(A, A.k_stride)) &&
+                  REC_IN_BOUNDS(static_cast<const T *>(A.q), qp, kn, key_extent(A, A.q_stride)) &&
+                  (!KDA || REC_IN_BOUNDS(A.g, gp + c, kn, gate_extent(A, KDA)))))
+    return;
+  if (c < kRecCols && vn > 0 && !REC_IN_BOUNDS(static_cast<const T *>(A.v), vp, vn, value_extent(A))) return;
+  if (!(KDA || REC_IN_BOUNDS(A.g, gp, 1, gate_extent(A, KDA))) ||
+      !REC_IN_BOUNDS(A.beta, A.beta + t * A.Hv + h, 1, int64_t(A.T) * A.Hv))
+    return;
   if (A.vec) {
     if (c < A.dk) {
       copy_async(reinterpret_cast<T *>(R.k[m]) + c, kp, 4 * sizeof(T));
@@ -325,7 +352,9 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
     for (int i = 0; i < NP * 4; ++i) {
       const int j = 32 * (i >> 2) + (i & 3);            // row less g4
       if (!FULL) S[i][0] = S[i][1] = pair(0.f, 0.f);
-      if (FULL || (col_ok && j + g4 < dk)) load_pairs(FULL ? st + j * dv : src, S[i]);
+      if ((FULL || (col_ok && j + g4 < dk)) &&
+          REC_IN_BOUNDS(static_cast<ST *>(A.pool), FULL ? st + j * dv : src, 4, pool_extent(A)))
+        load_pairs(FULL ? st + j * dv : src, S[i]);
       if (!FULL) {
         src += ((i & 3) == 3 ? 29 : 1) * dv;
         asm volatile("" : "+l"(src));
@@ -355,7 +384,9 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
     if (tid == 0 && A.status) atomicOr(A.status, kErrBadSeqlens);
     const float nan = __int_as_float(0x7fffffff);
     if (col_ok && g4 == 0)
-      for (int t = 0; t < len; ++t) st4(o + t * o_stride + cl, make_float4(nan, nan, nan, nan));
+      for (int t = 0; t < len; ++t)
+        if (REC_IN_BOUNDS(static_cast<T *>(A.o), o + t * o_stride + cl, 4, out_extent(A)))
+          st4(o + t * o_stride + cl, make_float4(nan, nan, nan, nan));
     return;
   }
   relate<KDA>(sm.rows[0], sm.coef[0], warp, n0, lane);
@@ -451,7 +482,8 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
           float y = z[m];
 #pragma unroll
           for (int l = 0; l <= m; ++l) y += C.P[m][l] * sm.u[l][c];
-          o[(p0 + m) * o_stride + c] = from_f32<T>(y);
+          if (REC_IN_BOUNDS(static_cast<T *>(A.o), o + (p0 + m) * o_stride + c, 1, out_extent(A)))
+            o[(p0 + m) * o_stride + c] = from_f32<T>(y);
         }
     }
     if (kStep && (n1 > 0 || p1 == keep)) {
@@ -502,7 +534,9 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
 #pragma unroll
       for (int i = 0; i < NP * 4; ++i) {
         const int j = 32 * (i >> 2) + (i & 3);
-        if (FULL || (col_ok && j + g4 < dk)) store_pairs(FULL ? st + j * dv : dst, S[i]);
+        if ((FULL || (col_ok && j + g4 < dk)) &&
+            REC_IN_BOUNDS(static_cast<ST *>(A.pool), FULL ? st + j * dv : dst, 4, pool_extent(A)))
+          store_pairs(FULL ? st + j * dv : dst, S[i]);
         if (!FULL) {
           dst += ((i & 3) == 3 ? 29 : 1) * dv;
           asm volatile("" : "+l"(dst));
@@ -593,14 +627,22 @@ __global__ void __launch_bounds__(32 * kOneWarps<ST, FULL>, 16 / kOneWarps<ST, F
   const int keep = A.keep ? A.keep[n] : 1;
   const bool fresh = A.reset && A.reset[n];
   float kv = 0.f, qv = 0.f, av = 1.f, vv = 0.f;    // thread c < 128: channel c
+  const int64_t head = int64_t(n) * A.Hv + h;
   if (tid < dk) {
-    kv = to_f32(static_cast<const T *>(A.k)[n * A.k_stride + int64_t(hk) * dk + tid]);
-    qv = to_f32(static_cast<const T *>(A.q)[n * A.q_stride + int64_t(hk) * dk + tid]);
-    if (KDA) av = A.g[(int64_t(n) * A.Hv + h) * dk + tid];
+    const int64_t ki = n * A.k_stride + int64_t(hk) * dk + tid, qi = n * A.q_stride + int64_t(hk) * dk + tid;
+    if (GDN_IN_BOUNDS(A.status, ki, key_extent(A, A.k_stride))) kv = to_f32(static_cast<const T *>(A.k)[ki]);
+    if (GDN_IN_BOUNDS(A.status, qi, key_extent(A, A.q_stride))) qv = to_f32(static_cast<const T *>(A.q)[qi]);
+    if (KDA && GDN_IN_BOUNDS(A.status, head * dk + tid, gate_extent(A, KDA))) av = A.g[head * dk + tid];
   }
-  if (tid < dv) vv = to_f32(static_cast<const T *>(A.v)[n * A.v_stride + int64_t(h) * dv + tid]);
-  const float gate = KDA ? 0.f : A.g[int64_t(n) * A.Hv + h];
-  const float beta = A.beta[int64_t(n) * A.Hv + h];
+  if (tid < dv) {
+    const int64_t vi = n * A.v_stride + int64_t(h) * dv + tid;
+    if (GDN_IN_BOUNDS(A.status, vi, value_extent(A))) vv = to_f32(static_cast<const T *>(A.v)[vi]);
+  }
+  float gate = 0.f, beta = 0.f;
+  if (GDN_IN_BOUNDS(A.status, head, int64_t(A.T) * A.Hv)) {
+    if (!KDA) gate = A.g[head];
+    beta = A.beta[head];
+  }
   if (slot < 0) return;
   bool bad = slot >= A.num_slots || keep < 0 || keep > 1;
 
@@ -616,7 +658,8 @@ __global__ void __launch_bounds__(32 * kOneWarps<ST, FULL>, 16 / kOneWarps<ST, F
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
     S[r].zero();
-    if ((FULL || (col_ok && row0 + r * W * RPW < dk)) && !bad && !fresh)
+    if ((FULL || (col_ok && row0 + r * W * RPW < dk)) && !bad && !fresh &&
+        REC_IN_BOUNDS(static_cast<ST *>(A.pool), FULL ? st + r * step : src, V, pool_extent(A)))
       S[r].load(FULL ? st + r * step : src);
     if (!FULL) {
       src += step;
@@ -633,10 +676,11 @@ __global__ void __launch_bounds__(32 * kOneWarps<ST, FULL>, 16 / kOneWarps<ST, F
     if (KDA) { as[tid] = a; ka[tid] = a * kv; qa[tid] = a * qv; }
   }
   bad = __syncthreads_or(bad);
-  T *o = static_cast<T *>(A.o) + (int64_t(n) * A.Hv + h) * dv;
+  T *o = static_cast<T *>(A.o) + head * dv;
+  const bool o_ok = tid < dv && GDN_IN_BOUNDS(A.status, head * dv + tid, out_extent(A));
   if (bad) {
     if (tid == 0 && A.status) atomicOr(A.status, kErrBadSeqlens);
-    if (tid < dv) o[tid] = from_f32<T>(__int_as_float(0x7fffffff));
+    if (o_ok) o[tid] = from_f32<T>(__int_as_float(0x7fffffff));
     return;
   }
   if (warp == 0) {
@@ -692,7 +736,7 @@ __global__ void __launch_bounds__(32 * kOneWarps<ST, FULL>, 16 / kOneWarps<ST, F
     for (int w = 0; w < W; ++w) { xs += xpart[w][tid]; ys += ypart[w][tid]; }
     const float u = beta * (vv - alpha * xs);
     us[tid] = u;
-    if (tid < dv) o[tid] = from_f32<T>(alpha * ys + kq_s * u);
+    if (o_ok) o[tid] = from_f32<T>(alpha * ys + kq_s * u);
   }
   if (keep == 0) return;
   __syncthreads();
@@ -711,7 +755,9 @@ __global__ void __launch_bounds__(32 * kOneWarps<ST, FULL>, 16 / kOneWarps<ST, F
 #pragma unroll
     for (int i = 0; i < V / 2; ++i)   // products and sum rounded each: see kStep
       s[i] = add2_apart(mul2(aa, S[r].get(i)), mul2(u2[i], kk));
-    if (FULL || (col_ok && j < dk)) Piece<ST>::store(FULL ? st + r * step : dst, s);
+    if ((FULL || (col_ok && j < dk)) &&
+        REC_IN_BOUNDS(static_cast<ST *>(A.pool), FULL ? st + r * step : dst, V, pool_extent(A)))
+      Piece<ST>::store(FULL ? st + r * step : dst, s);
     if (!FULL) {
       dst += step;
       asm volatile("" : "+l"(dst));

@@ -162,10 +162,12 @@ int gdn_chunk_fwd_noalloc(const void *q, const void *k, const void *v, const flo
                           void *stream);
 
 /* 1 if this library was built with device-side bounds checks (-DGDN_CHECKS=1),
- * else 0. In a checked build the tensor-core chunked forward pass (chunk map,
- * prep, state scan, segment composition) compares every plain global-memory
- * index with the extent of its buffer before the access; an index outside it
- * skips the access and records GDN_ERR_DEVICE_BOUNDS for gdn_get_status. (TMA
+ * else 0. In a checked build the tensor-core chunked passes (chunk map, prep,
+ * state scan, segment composition, chunkwise backward) and the pooled recurrent
+ * rule compare every plain global-memory index of rows, gates, states and outputs
+ * with the extent of its buffer before the access; an index outside it skips the
+ * access and records GDN_ERR_DEVICE_BOUNDS for gdn_get_status (of the workspace,
+ * or of the pooled rule's status block). (TMA
  * copies need no check: the hardware clips them to the tensor map.) It is
  * the stand-in for a memory checker when none is available; it is slower and
  * not meant for production. */
