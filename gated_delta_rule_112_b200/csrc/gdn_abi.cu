@@ -312,6 +312,9 @@ int gdn_get_status(void *workspace, void *stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(s) != cudaSuccess) return GDN_ERR_CUDA;
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+#if GDN_CHECKS
+  if (!workspace) workspace = qk_checked_block();
+#endif
   if (!workspace) return GDN_OK;
   uint32_t err = 0;
   if (cudaMemcpy(&err, workspace, sizeof(err), cudaMemcpyDeviceToHost) != cudaSuccess)

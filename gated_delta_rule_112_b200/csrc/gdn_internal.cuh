@@ -179,6 +179,12 @@ cudaError_t launch_chunk_tc(const void *q, const void *k, const void *v, const f
                             const float *beta, const float *s0, int B, int T, int H, int N,
                             void *o, float *sN, void *ws, const WsLayout &L, cudaStream_t s,
                             __nv_bfloat16 *s_chunks = nullptr);
+// Where the query/key norms, which have no workspace or status block of their
+// own, record an index outside its buffer in checked builds (null if the
+// device's memory cannot be had).
+#if GDN_CHECKS
+void *qk_checked_block();
+#endif
 // channel_gate: g is [N, H, d_k] (one log-decay per d_k channel), else [N, H].
 cudaError_t launch_decode(const void *q, const void *k, const void *v, const float *g,
                           const float *beta, float *state, void *o, int N, int H, int dk, int dv,

@@ -50,6 +50,13 @@
 namespace gdn {
 namespace {
 
+// What bounds checks need beside the kernels' own arguments (GDN_CHECKS builds).
+#if GDN_CHECKS
+#define QK_CHECKED(...) __VA_ARGS__
+#else
+#define QK_CHECKED(...)
+#endif
+
 constexpr int kQkThreads = 256;
 constexpr int kMaxD = 256;
 constexpr int kBlocksPerSm = 2;
@@ -83,6 +90,7 @@ struct QkArgs {
   int lg;                         // log2 of the lanes of a row
   int rpi, splits;                // rows an item, items a token
   float eps, w0, rope_scale, inv_n;
+  QK_CHECKED(uint32_t *err; int64_t dw_extent;)
 };
 
 // A lane's place in a row: chunks of E elements at a and b, of which na and nb
@@ -284,10 +292,40 @@ struct Rows {
   }
   __device__ __forceinline__ P *first(int h) const { return at(a, h, hs); }
   __device__ __forceinline__ P *second(int h) const { return at(b, h, hs); }
+  // Whether what a lane's access to row h touches lies in the buffer.
+  QK_CHECKED(const P *base; int64_t extent; uint32_t *err;)
+  template <int E, int ACC>
+  __device__ __forceinline__ bool in_bounds(int h, const Lane &L, bool reads) const {
+#if GDN_CHECKS
+    const int na = reads && ACC >= E ? E : L.na, nb = reads && ACC >= E ? E : L.nb;
+    return (na == 0 || GDN_IN_BOUNDS(err, first(h) - base, extent - na + 1)) &&
+           (nb == 0 || GDN_IN_BOUNDS(err, second(h) - base, extent - nb + 1));
+#else
+    return true;
+#endif
+  }
 };
+#if GDN_CHECKS
+template <typename P>
+__device__ __forceinline__ void bound(Rows<P> &r, const QkArgs &A, const void *base, int64_t extent) {
+  r.base = static_cast<const P *>(base);
+  r.extent = extent;
+  r.err = A.err;
+}
+// Elements from the first of a part's rows to the last; strides in bytes.
+template <typename P>
+__device__ __forceinline__ void bound(Rows<P> &r, const QkArgs &A, const void *base, int64_t ts, int64_t hs,
+                                      int H) {
+  bound(r, A, base, (int64_t(A.T - 1) * ts + int64_t(H - 1) * hs) / int64_t(sizeof(P)) + A.d);
+}
+#endif
 template <int E, int ACC, typename T>
 __device__ __forceinline__ void load_row(const Rows<const T> &P, int h, const Lane &L, Raw<T, E> &r) {
   constexpr int half = sizeof(r.w) / sizeof(r.w[0]) / 2;
+  if (!P.template in_bounds<E, ACC>(h, L, true)) {
+    r = Raw<T, E>{};
+    return;
+  }
   if (ACC == 8 && E == 4 && sizeof(T) == 2) {        // side by side (see with_variant)
     const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(P.first(h)));
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -374,7 +412,7 @@ __device__ __forceinline__ void turn(const QkArgs &A, const Lane &L, float *row,
 // 3e8 turns, seven times fp32's own rounding.
 __device__ __forceinline__ void make_angles(const QkArgs &A, int t, int lane, int pairs, float *cs) {
   constexpr double kInv2Pi = 0.15915494309189535, kInv2PiRest = -9.839338337591243e-18;   // 1 / (2 pi)
-  const double p = double(A.pos[t]);
+  const double p = GDN_IN_BOUNDS(A.err, t, A.T) ? double(A.pos[t]) : 0.0;
   __syncwarp();
   for (int j = lane; j < pairs; j += 32) {
     float s = 0.f, c = 1.f;
@@ -466,8 +504,10 @@ template <typename T, bool PACKED, int E, int PAIR, int ACC>
 struct Source {
   using Data = Raw<T, E>;
   Rows<const T> rows;
-  __device__ __forceinline__ Source(const QkArgs &, const Part &P, int64_t t, const Lane &L)
-      : rows(static_cast<const T *>(P.x), t * P.x_ts, P.x_hs, L, true) {}
+  __device__ __forceinline__ Source(const QkArgs &A, const Part &P, int64_t t, const Lane &L)
+      : rows(static_cast<const T *>(P.x), t * P.x_ts, P.x_hs, L, true) {
+    QK_CHECKED(bound(rows, A, P.x, P.x_ts, P.x_hs, P.H);)
+  }
   __device__ __forceinline__ void load(int h, const Lane &L, Data &r) const {
     load_row<E, ACC>(rows, h, L, r);
   }
@@ -484,11 +524,20 @@ struct Source<T, true, E, PAIR, ACC> {
     e = P.x_scales + t * P.H * blocks;
     ea = L.na > 0 ? L.a / 32 : 0;
     eb = L.nb > 0 ? L.b / 32 : 0;
+    QK_CHECKED(bound(rows, A, P.x, int64_t(A.T) * P.H * A.d); scales = P.x_scales;
+               scales_extent = int64_t(A.T) * P.H * blocks;)
   }
+  QK_CHECKED(const uint8_t *scales; int64_t scales_extent;)
   __device__ __forceinline__ void load(int h, const Lane &L, Data &r) const {
+    const uint8_t *s = e + int64_t(h) * blocks;
+    if (!rows.template in_bounds<E, ACC>(h, L, true) ||
+        !GDN_IN_BOUNDS(rows.err, s + ea - scales, scales_extent) ||
+        !GDN_IN_BOUNDS(rows.err, s + eb - scales, scales_extent)) {
+      r = Codes<E>{};
+      return;
+    }
     load_chunk<E, ACC>(rows.first(h), L.na, r.w);
     load_chunk<E, ACC>(rows.second(h), L.nb, r.w + E / 4);
-    const uint8_t *s = e + int64_t(h) * blocks;
     r.ea = s[ea];
     r.eb = PAIR == kPairSplit ? s[eb] : r.ea;        // side by side, both are of one block
   }
@@ -615,7 +664,7 @@ __device__ __forceinline__ void write_codes(const QkArgs &A, const Rows<uint8_t>
   }
   if ((L.a & 31) == 0 && L.na > 0) scales[L.a / 32] = uint8_t(ea);
   if (PAIR == kPairSplit && (L.b & 31) == 0 && L.nb > 0) scales[L.b / 32] = uint8_t(eb);
-  if (!on) return;
+  if (!on || !codes.template in_bounds<E, ACC>(h, L, false)) return;
   store_codes<E, ACC>(codes.first(h), L.na, c);
   store_codes<E, ACC>(codes.second(h), L.nb, c + E / 4);
 }
@@ -664,9 +713,11 @@ __global__ void __launch_bounds__(kQkThreads, kBlocksPerSm) gdn_qk_fwd_kernel(co
       factors<E, PAIR>(A, L, l, cs, w_all[part], 1.f, C, S);
       using Src = Source<T, PACKED, E, PAIR, ACC>;
       const Src src(A, P, I.t, L);
-      const Rows<T> out(static_cast<T *>(P.out), I.t * P.out_ts, P.out_hs, L, false);
+      Rows<T> out(static_cast<T *>(P.out), I.t * P.out_ts, P.out_hs, L, false);
       const int64_t row0 = int64_t(I.t) * P.H;
-      const Rows<uint8_t> codes(P.codes, row0 * A.d, A.d, L, false);
+      Rows<uint8_t> codes(P.codes, row0 * A.d, A.d, L, false);
+      QK_CHECKED(bound(out, A, P.out, P.out_ts, P.out_hs, P.H);
+                 bound(codes, A, P.codes, int64_t(A.T) * P.H * A.d);)
       for (int h = h0 + sub; h - sub < h1; h += R * U) {
         typename Src::Data raw[U];
 #pragma unroll
@@ -696,7 +747,7 @@ __global__ void __launch_bounds__(kQkThreads, kBlocksPerSm) gdn_qk_fwd_kernel(co
               x.v[i] = mul2(x.v[i], i < E / 2 || !PACKED ? pair(sc.a, sc.a) : pair(sc.b, sc.b));
           }
           turn<E, PAIR>(A, L, row_buf, C, S, x);
-          if (on && (!PACK || P.out)) {
+          if (on && (!PACK || P.out) && out.template in_bounds<E, ACC>(h + u * R, L, false)) {
             store_chunk<E, ACC>(out.first(h + u * R), L.na, x.v);
             store_chunk<E, ACC>(out.second(h + u * R), L.nb, x.v + E / 2);
           }
@@ -707,7 +758,8 @@ __global__ void __launch_bounds__(kQkThreads, kBlocksPerSm) gdn_qk_fwd_kernel(co
           const int h_first = h - sub, bytes = min(R * U, h1 - h_first) * blocks;
           __syncwarp();
           for (int i = lane; i < bytes; i += 32)
-            P.scales[(row0 + h_first) * blocks + i] = exps[i];
+            if (GDN_IN_BOUNDS(A.err, (row0 + h_first) * blocks + i, int64_t(A.T) * P.H * blocks))
+              P.scales[(row0 + h_first) * blocks + i] = exps[i];
           __syncwarp();
         }
       }
@@ -756,8 +808,9 @@ __global__ void __launch_bounds__(WEIGHTS ? kQkThreads : kPlainBwdThreads,
       }
       using Src = Source<T, PACKED, E, PAIR, ACC>;
       const Src src(A, P, I.t, L);
-      const Rows<const DT> dy(static_cast<const DT *>(P.dy), I.t * P.dy_ts, P.dy_hs, L, true);
-      const Rows<T> out(static_cast<T *>(P.out), I.t * P.out_ts, P.out_hs, L, false);
+      Rows<const DT> dy(static_cast<const DT *>(P.dy), I.t * P.dy_ts, P.dy_hs, L, true);
+      Rows<T> out(static_cast<T *>(P.out), I.t * P.out_ts, P.out_hs, L, false);
+      QK_CHECKED(bound(dy, A, P.dy, P.dy_ts, P.dy_hs, P.H); bound(out, A, P.out, P.out_ts, P.out_hs, P.H);)
       for (int h = h0 + sub; h - sub < h1; h += R * U) {
         typename Src::Data raw[U];
         Raw<DT, E> grad[U];
@@ -797,7 +850,7 @@ __global__ void __launch_bounds__(WEIGHTS ? kQkThreads : kPlainBwdThreads,
             if (WEIGHTS && on) dw[part].v[i] = fma2(z.v[i], hx, dw[part].v[i]);
             x.v[i] = A.norm == GDN_NORM_NONE ? dh.v[i] : mul2(fma2(hx, mm, dh.v[i]), rr);
           }
-          if (on) {
+          if (on && out.template in_bounds<E, ACC>(h + u * R, L, false)) {
             store_chunk<E, ACC>(out.first(h + u * R), L.na, x.v);
             store_chunk<E, ACC>(out.second(h + u * R), L.nb, x.v + E / 2);
           }
@@ -819,7 +872,8 @@ __global__ void __launch_bounds__(WEIGHTS ? kQkThreads : kPlainBwdThreads,
       for (int e = threadIdx.x; e < A.d; e += kThreads) {
         float s = 0.f;
         for (int i = 0; i < kWarps * R; ++i) s += rows_all[i / R][(i % R) * G * 2 * E + e];
-        A.dw_part[(int64_t(part) * gridDim.x + blockIdx.x) * A.d + e] = s;
+        if (GDN_IN_BOUNDS(A.err, (int64_t(part) * gridDim.x + blockIdx.x) * A.d + e, A.dw_extent))
+          A.dw_part[(int64_t(part) * gridDim.x + blockIdx.x) * A.d + e] = s;
       }
     }
   }
@@ -966,6 +1020,7 @@ int fill(QkArgs &A, const gdn_qk_params *p, const gdn_rows *const x[2],
          const gdn_packed *const x8[2], const gdn_rows *const dy[2], size_t dye,
          const gdn_rows *const out[2], const gdn_packed *const out8[2]) {
   const size_t e = p->dtype == GDN_BF16 ? 2 : 4;
+  QK_CHECKED(A.err = static_cast<uint32_t *>(qk_checked_block());)
   A.pos = p->positions;
   A.inv_freq = p->inv_freq;
   A.T = p->T; A.d = p->d; A.rot = p->rot; A.norm = p->norm;
@@ -1041,6 +1096,7 @@ int run_bwd(const gdn_qk_params *p, const gdn_rows *const dy[2], int grad_dtype,
   rc = fill(A, p, x, PACKED ? x8 : nullptr, dy, grad_dtype == GDN_BF16 ? 2 : 4, out, nullptr);
   if (rc != GDN_OK) return rc;
   A.dw_part = static_cast<float *>(ws);
+  QK_CHECKED(A.dw_extent = ws_bytes / sizeof(float);)
   const unsigned grid = dw_q || dw_k ? plan(A, kBwdE, kQkThreads, kBlocksPerSm)
                                      : plan(A, kBwdE, kPlainBwdThreads, kPlainBwdBlocksPerSm);
   const int acc = access_width(A, p->dtype == GDN_BF16 ? 2 : 4, grad_dtype == GDN_BF16 ? 2 : 4, PACKED);
@@ -1059,6 +1115,16 @@ int run_bwd(const gdn_qk_params *p, const gdn_rows *const dy[2], int grad_dtype,
 }
 
 }  // namespace
+
+#if GDN_CHECKS
+namespace {
+__device__ uint32_t g_checked[64];
+}
+void *qk_checked_block() {
+  void *p = nullptr;
+  return cudaGetSymbolAddress(&p, g_checked) == cudaSuccess ? p : nullptr;
+}
+#endif
 }  // namespace gdn
 
 using namespace gdn;

@@ -163,11 +163,12 @@ int gdn_chunk_fwd_noalloc(const void *q, const void *k, const void *v, const flo
 
 /* 1 if this library was built with device-side bounds checks (-DGDN_CHECKS=1),
  * else 0. In a checked build the tensor-core chunked passes (chunk map, prep,
- * state scan, segment composition, chunkwise backward) and the pooled recurrent
- * rule compare every plain global-memory index of rows, gates, states and outputs
- * with the extent of its buffer before the access; an index outside it skips the
- * access and records GDN_ERR_DEVICE_BOUNDS for gdn_get_status (of the workspace,
- * or of the pooled rule's status block). (TMA
+ * state scan, segment composition, chunkwise backward), the pooled recurrent rule
+ * and the query/key norms compare every plain global-memory index of rows, gates,
+ * states, codes and outputs with the extent of its buffer before the access; an
+ * index outside it skips the access and records GDN_ERR_DEVICE_BOUNDS for
+ * gdn_get_status (of the workspace, of the pooled rule's status block, or of NULL
+ * for the norms). (TMA
  * copies need no check: the hardware clips them to the tensor map.) It is
  * the stand-in for a memory checker when none is available; it is slower and
  * not meant for production. */
@@ -560,7 +561,8 @@ int gdn_selftest_wait_timeout(void *workspace, void *stream);
  * gdn_get_status -- synchronises `stream`, then reports the first error seen:
  * GDN_ERR_CUDA for a failed kernel, or the code a gdn_chunk_fwd kernel left in
  * `workspace` (GDN_ERR_DEVICE_TIMEOUT, GDN_ERR_INVALID_ARG for bad
- * cu_seqlens). Clears the device error word. `workspace` may be NULL.
+ * cu_seqlens). Clears the device error word. `workspace` may be NULL; a checked
+ * build then reports what the query/key norms recorded on the current device.
  */
 int gdn_get_status(void *workspace, void *stream);
 

@@ -1,6 +1,7 @@
-"""The bounds-checked build (libgdn_checked.so) on the pooled recurrent rule: every index of q, k, v, the gates,
-the pool and the outputs is compared with its buffer's extent before the access. The cases run in a fresh
-process; no call may record an index outside (gdn_get_status == GDN_OK), and all must match the oracle."""
+"""The bounds-checked build (libgdn_checked.so) on the pooled recurrent rule and the query/key norms: every index
+of rows, gates, states, codes and outputs is compared with its buffer's extent before the access. The cases run
+in a fresh process; no call may record an index outside (gdn_get_status == GDN_OK), and all must match the
+oracle or the formulas."""
 import os
 import subprocess
 import sys
@@ -46,6 +47,36 @@ def _recurrent_cases():
     print("checked build: all cases clean")
 
 
+def _norm_cases():
+    import torch
+
+    import gated_delta_rule_112_b200 as gdn
+    from tests import test_qk_norm_gpu as t
+
+    assert gdn.lib().gdn_checked_build() == 1, "not the checked library"
+
+    def clean(what):
+        code = gdn.get_status()
+        assert code == gdn.OK, (what, gdn.lib().gdn_status_string(code))
+
+    for case in range(len(t.CASES)):
+        t.test_forward(case)
+        clean(("forward", case))
+        t.test_codes_are_exact(case)
+        clean(("codes", case))
+        t.test_backward(case, t.F)
+        t.test_backward(case, None)
+        clean(("backward", case))
+        t.test_from_the_checkpoint(case)
+        clean(("from the checkpoint", case))
+    for test in (t.test_strided_unaligned_and_in_place, t.test_heads_outermost, t.test_no_tokens_and_one_tensor,
+                 t.test_codes_at_the_ends):
+        test()
+        clean(test.__name__)
+    torch.cuda.synchronize()
+    print("checked build: all cases clean")
+
+
 def _run(what):
     from gated_delta_rule_112_b200 import build as gbuild
     env = dict(os.environ, GDN_LIBRARY=gbuild.build(checked=True), PYTHONPATH=ROOT)
@@ -60,6 +91,11 @@ def test_checked_build_runs_the_pooled_rule_clean():
     _run("recurrent")
 
 
+@pytest.mark.gpu
+def test_checked_build_runs_the_norms_clean():
+    _run("norms")
+
+
 if __name__ == "__main__":
     sys.path.insert(0, ROOT)
-    {"recurrent": _recurrent_cases}[sys.argv[1]]()
+    {"recurrent": _recurrent_cases, "norms": _norm_cases}[sys.argv[1]]()
