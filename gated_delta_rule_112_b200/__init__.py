@@ -638,7 +638,10 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, w_q=None, w_k=None, positions=None, i
     were, or ``Packed``: then at the point the 8-bit rows stand for). dq_out,
     dk_out: gradients of its outputs (fp32, or the rows' dtype). Returns a dict:
     dq, dk (the rows' dtype; for packed rows ``dtype``, bfloat16 if not given),
-    dw_q, dw_k ([d] fp32, None without weights). out: ``(dq, dk)`` to write."""
+    dw_q, dw_k ([d] fp32, None without weights). out: ``(dq, dk)`` to write; each
+    may be its own raw rows, or its gradients if they have the rows' type. Rows
+    may not overlap, so a broadcast gradient (of a sum, say) is refused: give a
+    ``.contiguous()`` one."""
     name = "gdn_qk_norm_rope_bwd"
     packed, qx, kx = _qk_source(name, q, k)
     dev = qx.get_device()
@@ -732,7 +735,8 @@ def chunk_fwd_packed(q, k, v, g, beta, initial_state=None, cu_seqlens=None, chun
                      output_final_state=True, stream=None, **norm):
     """``qk_norm_rope_fwd`` (its keywords in ``norm``; positions [B*T]) and
     ``chunk_fwd`` of the result, keeping q, k and v in 8 bits for
-    ``chunk_bwd_packed``. q, k, v: [B,T,H,d]. Returns ``(o, final_state or None,
+    ``chunk_bwd_packed``. q, k, v: [B,T,H,d] of one type, with equally many heads
+    (repeat q and k where value heads share them). Returns ``(o, final_state or None,
     Checkpoint)``; o and the state are those of the exact q, k, v."""
     dev = q.get_device()
     if dev < 0 or stream is not None or dev != torch.cuda.current_device():

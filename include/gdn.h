@@ -425,17 +425,22 @@ int gdn_chunk_bwd_exact(const void *q, const void *k, const void *v, const float
  *              by running them after the accepted ones with keep at the latter.
  *   reset      bytes [N] or NULL: non-zero starts run n from a zero state
  *              instead of what its slot holds.
- *   o          [T, H_v, d_v] (dtype), contiguous, aligned to four elements.
+ *   o          [T, H_v, d_v] (dtype), contiguous, aligned to four elements,
+ *              not overlapping an input.
  *   status     NULL, or a 256-byte control block, zeroed by the caller before
  *              its first use, for gdn_get_status(status, stream).
- * A slot that two runs name, when either stores its state, a slot outside the
- * pool, a keep outside [0, length] and tokens outside [0, T] are found on the
- * device: that run's state is left alone, its outputs (unless its tokens are
- * the bad part) are NaN, and the status is GDN_ERR_INVALID_ARG. Runs that keep
- * nothing may share a slot. Boundaries that go backwards make runs overlap:
- * outputs of the shared tokens are then undefined. d_k, d_v <= 128, d_v a
- * multiple of 4, H_v < 2^20, N * H_v < 2^30. No workspace; the call can be
- * captured, and calls on disjoint slots may overlap.
+ * Of runs that have tokens, a slot that two name, when either stores its state, a
+ * slot outside the pool and a keep outside [0, length] are found on the device,
+ * and of all runs but padding tokens outside [0, T]: that run's state is left
+ * alone, its outputs (unless its tokens are the bad part) are NaN, and the status
+ * is GDN_ERR_INVALID_ARG. Runs that keep nothing may share a slot. Boundaries that
+ * go backwards make runs overlap: outputs of the shared tokens are then undefined.
+ * d_k, d_v <= 128, d_v a multiple of 4, H_v < 2^20, N * H_v < 2^30. No workspace;
+ * the call can be captured, and calls on disjoint slots may overlap. Every run
+ * looks through all slots for its own, once a head or half a head (H_v or 2 H_v
+ * times N^2 reads of 4 bytes, from L2): nothing beside the states of some hundreds
+ * of runs, but for 16,384 runs of 32 heads half as many bytes as their fp32 states
+ * of d = 128.
  */
 int gdn_recurrent_fwd(const void *q, const void *k, const void *v, const float *g,
                       const float *beta, void *pool, const int32_t *slots,
@@ -527,7 +532,9 @@ size_t gdn_qk_norm_rope_bwd_workspace_size(const gdn_qk_params *p);
  * dw_k ([d] fp32, wanted exactly when w_q, w_k are given) for gradients dq_out,
  * dk_out of the outputs, which have grad_dtype (GDN_F32, as gdn_chunk_bwd
  * leaves them, or dtype). The weights' gradients are summed in a fixed order.
- * workspace: 256-byte aligned, not shared with a concurrent call.
+ * workspace: 256-byte aligned, not shared with a concurrent call. dq (dk) may be
+ * the raw rows themselves, or the gradients where they have its type (same data and
+ * strides); otherwise outputs overlap nothing.
  */
 int gdn_qk_norm_rope_bwd(const gdn_qk_params *p, const gdn_rows *dq_out, const gdn_rows *dk_out,
                          int grad_dtype, const gdn_rows *q, const gdn_rows *k, const gdn_rows *dq,

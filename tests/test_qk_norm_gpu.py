@@ -610,3 +610,31 @@ def test_training_step_with_states_weights_and_boundaries(kind):
         assert off <= b * float((r * weight.abs()).max()) * dz + tol(dtype) * np.linalg.norm(dx), (n, off)
         off = np.linalg.norm(np64(out["dw_" + n[1]]) - dw)
         assert off <= (b + TOL_F32) * dz * float(h.square().sum((0, 1)).max().sqrt()), (n, off)
+
+
+@pytest.mark.parametrize("weights", [False, True])
+def test_gradients_written_over_their_inputs(weights):
+    """dq, dk in the place of the raw rows, and in the place of the gradients that they come from."""
+    import gated_delta_rule_112_b200 as gdn
+    for T, Hq, Hk, d, rot, inter in ((37, 5, 3, 128, 64, False), (2000, 3, 1, 96, 96, True), (9, 7, 2, 33, 2, False)):
+        q, k, w, how = make(T, Hq, Hk, d, BF, rot, "l2", weights, inter, seed=65)
+        gen = torch.Generator().manual_seed(66)
+        dy = [torch.randn(x.shape, generator=gen).to(BF) for x in (q, k)]
+        kw = dev(how, w)
+        ref = gdn.qk_norm_rope_bwd(dy[0].cuda(), dy[1].cuda(), q.cuda(), k.cuda(), **kw)
+        for over in ("rows", "gradients"):
+            x, g = [q.cuda(), k.cuda()], [y.cuda() for y in dy]
+            into = x if over == "rows" else g
+            out = gdn.qk_norm_rope_bwd(*g, *x, out=tuple(into), **kw)
+            assert out["dq"].data_ptr() == into[0].data_ptr()
+            assert all(torch.equal(out[n], ref[n]) for n in ref if ref[n] is not None)
+
+
+def test_broadcast_gradients_are_refused():
+    import gated_delta_rule_112_b200 as gdn
+    q = torch.randn(6, 2, 64, generator=torch.Generator().manual_seed(67)).cuda()
+    for dy in (torch.ones(6, 1, 64).cuda().expand(6, 2, 64), torch.ones(1, 2, 64).cuda().expand(6, 2, 64)):
+        with pytest.raises(gdn.GdnError):
+            gdn.qk_norm_rope_bwd(dy, None, q, None)
+    with pytest.raises(ValueError):
+        gdn.qk_norm_rope_bwd(torch.ones((), device="cuda").expand(6, 2, 64), None, q, None)
