@@ -942,25 +942,41 @@ unsigned plan(QkArgs &A, int e, int threads, int per_sm) {
 
 // Turns the run-time choices into template arguments. Accesses of eight
 // elements: a chunk of eight (E = 8), or two chunks of four side by side.
+//
+// Measured for 16384 x 32 rows of 128, in us. The common width of a head, 65 to
+// 128 elements, is known to the compiler where the accesses are wide. That pays
+// in the backward kernels (92 against 97 without weights and 103 against 112 with
+// them, 103 against 117 from codes, fp32 rows 117 against 126) and a little in
+// the forward ones (46.5 against 47.4, with codes 68 against 70, fp32 rows 0 to 3
+// %). Eight elements an access instead of four, width unknown: forward 47 against
+// 50 (interleaved 50 against 56, with codes 70 against 77); in the backward
+// kernels nothing (112.3 against 112.3, and within 0.5 % for rows of 64, 192 and
+// 256) but for bf16 rows with halves through shared memory (111 against 113), so
+// there it comes with the known width or with those.
 template <int V> struct Const { static constexpr int value = V; };
 template <int E, typename F>
 void with_variant(int pair, int acc, int lg, F f) {
-  // The common width of a head, 65 to 128 elements, is known to the compiler
-  // where the accesses are wide.
   constexpr int known = E == 8 ? 3 : 4;
   auto pick = [&](auto a, auto g) {
     constexpr int wide = decltype(a)::value, split = wide >= E ? E : 4;
     if (pair == kPairNone) f(Const<kPairNone>{}, a, g);
     else if (pair == kPairInterleaved) f(Const<kPairInterleaved>{}, a, g);
-    else if (pair == kPairSplit) f(Const<kPairSplit>{}, Const<split>{}, g);
-    else f(Const<kPairShared>{}, a, Const<0>{});
+    else f(Const<kPairSplit>{}, Const<split>{}, g);
   };
-  if (acc == 8 && lg == known) pick(Const<8>{}, Const<known>{});
-  else if (acc == 8) pick(Const<8>{}, Const<0>{});
-  else if (acc >= 4) pick(Const<4>{}, Const<0>{});
-  else if (pair == kPairNone) f(Const<kPairNone>{}, Const<1>{}, Const<0>{});
-  else if (pair == kPairInterleaved) f(Const<kPairInterleaved>{}, Const<1>{}, Const<0>{});
-  else f(Const<kPairShared>{}, Const<1>{}, Const<0>{});
+  if (pair == kPairShared) {
+    if (acc == 8) f(Const<kPairShared>{}, Const<8>{}, Const<0>{});
+    else if (acc >= 4) f(Const<kPairShared>{}, Const<4>{}, Const<0>{});
+    else f(Const<kPairShared>{}, Const<1>{}, Const<0>{});
+  } else if (acc == 8 && lg == known) {
+    pick(Const<8>{}, Const<known>{});
+  } else if (acc >= 4) {
+    if (E == 8 && acc == 8) pick(Const<E>{}, Const<0>{});
+    else pick(Const<4>{}, Const<0>{});
+  } else if (pair == kPairNone) {            // halves in chunks need accesses of four
+    f(Const<kPairNone>{}, Const<1>{}, Const<0>{});
+  } else {
+    f(Const<kPairInterleaved>{}, Const<1>{}, Const<0>{});
+  }
 }
 
 template <bool PACKED, bool PACK>
