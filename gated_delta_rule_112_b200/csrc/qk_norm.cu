@@ -27,10 +27,12 @@
 // 2 pi as a sum of two fp64 numbers, less its whole turns, so far positions lose
 // nothing; fp32 sine and cosine of the remainder follow.
 //
-// Measured (B200, 16384 tokens, 16 + 16 heads of d = 128, bf16): forward 46 us =
-// 89 % of the copy rate, gradients from fp32 ones 91 us = 90 %, forward with the
-// checkpoint 67 us = 77 %, gradients with weights from the checkpoint 103 us = 70
-// %. The first two wait for HBM; the 8-bit ones issue two to three instructions
+// Measured (B200, 16384 tokens, 16 + 16 heads of d = 128, bf16): forward 46.6 us
+// = 88 % of the copy rate, gradients from fp32 ones 92 us = 89 %, forward with the
+// checkpoint 68 us = 76 %, gradients with weights from the checkpoint 103 us = 70
+// %. fp32 rows: forward 97 us = 85 %, gradients 131 us = 94 %, but 171 us forward
+// with halves through shared memory, where a step's raw rows, 64 registers a lane,
+// spill. The first two wait for HBM; the 8-bit ones issue two to three instructions
 // an element pair and are bound by both. What brought them there from 83, 128,
 // 117 and 140 us: a pair's elements in one lane (no exchange), factors formed
 // once a token, paired multiply-adds, sixteen elements a lane, reads without

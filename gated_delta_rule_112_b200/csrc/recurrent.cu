@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
   ST *st = static_cast<ST *>(A.pool) + (int64_t(bad ? 0 : slot) * A.Hv + h) * dk * dv + col + g4 * dv;
   Pair S[NP * 4][2];
   // d_v known: the rows lie at constant offsets. Otherwise the pointer steps
-  // from row to row, kept from the compiler, which would hold them all.
+  // from row to row, kept from the compiler, which would hold them all (with d_k
+  // above 96 up to 16 bytes a thread are spilled all the same).
   if (bad || fresh) {
 #pragma unroll
     for (int i = 0; i < NP * 4; ++i) S[i][0] = S[i][1] = pair(0.f, 0.f);
@@ -779,8 +780,9 @@ cudaError_t launch_np(RecArgs &A, cudaStream_t s) {
 template <typename T, typename ST, bool KDA>
 cudaError_t launch_gate(RecArgs &A, cudaStream_t s) {
   // One token a run goes to its own kernel, where the rows come in whole pieces
-  // (170 us against 211 us for 256 x 32 fp32 states, 34 us against 64 us for 96
-  // x 32 bf16 ones by the kernel for runs).
+  // (169 us against 179 us for 256 x 32 fp32 states, 34 us against 49 us for 96
+  // x 32 bf16 ones by the kernel for runs). A call with boundaries never does: the
+  // lengths are on the device.
   if (!A.cu && A.L == 1 && A.dv % Piece<ST>::n == 0) {
     const dim3 units = grid_of(A, A.Hv);
     if (A.dk == 128 && A.dv == 128)
