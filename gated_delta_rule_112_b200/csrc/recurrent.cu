@@ -824,6 +824,8 @@ extern "C" int gdn_recurrent_fwd(const void *q, const void *k, const void *v, co
   if (!slots && N > num_slots) return GDN_ERR_INVALID_ARG;
   if (d_k > 128 || d_v > 128 || d_v % 4) return GDN_ERR_UNSUPPORTED;
   if (H_v >= 1 << 20 || int64_t(N) * H_v >= (int64_t(1) << 30)) return GDN_ERR_UNSUPPORTED;
+  // the search for a slot named twice: N reads a run and head (two seconds or so at the limit)
+  if (slots && double(N) * N * H_v > 4398046511104.0) return GDN_ERR_UNSUPPORTED;   // 2^42
   if (q_stride < int64_t(H_k) * d_k || k_stride < int64_t(H_k) * d_k ||
       v_stride < int64_t(H_v) * d_v)
     return GDN_ERR_INVALID_ARG;

@@ -440,7 +440,8 @@ int gdn_chunk_bwd_exact(const void *q, const void *k, const void *v, const float
  * looks through all slots for its own, once a head or half a head (H_v or 2 H_v
  * times N^2 reads of 4 bytes, from L2): nothing beside the states of some hundreds
  * of runs, but for 16,384 runs of 32 heads half as many bytes as their fp32 states
- * of d = 128.
+ * of d = 128. With slots, N^2 H_v is at most 2^42, which no pool of such states
+ * reaches.
  */
 int gdn_recurrent_fwd(const void *q, const void *k, const void *v, const float *g,
                       const float *beta, void *pool, const int32_t *slots,

@@ -285,3 +285,14 @@ def test_training_step_refuses_what_it_would_misread(L, monkeypatch, bad):
         ckpt = gdn.Checkpoint(p, p, p, (2, 3, 2, 128, 128), torch.bfloat16)
         with pytest.raises(ValueError):
             gdn.chunk_bwd_packed(ckpt, a["g"], a["beta"], d_o, **more, **last)
+
+
+@pytest.mark.parametrize("N,Hv,ok", [(1 << 21, 1, True), ((1 << 21) + 1, 1, False), (1 << 29, 1, False),
+                                     (370_727, 32, True), (370_728, 32, False)])
+def test_recurrent_refuses_a_search_without_end(L, N, Hv, ok):
+    """Every run reads all slots: half a thousand million of them would keep the GPU for days. T = 0 or no
+    slots leave nothing to search."""
+    how = dict(N=N, Hv=Hv, Hk=1, P=N, vs=128 * Hv, dk=128, dv=4)
+    code = recurrent(L, **how, T=0, cu=P)
+    assert code == (gdn.OK if ok else gdn.ERR_UNSUPPORTED)
+    assert recurrent(L, **how, T=0, cu=P, slots=None) == gdn.OK
