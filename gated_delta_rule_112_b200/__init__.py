@@ -761,7 +761,8 @@ def chunk_bwd_packed(ckpt: Checkpoint, g, beta, d_o, initial_state=None, cu_seql
     """Gradients of ``chunk_fwd_packed`` from its checkpoint, at the q, k and v
     that the 8-bit rows stand for. Arguments as there and for ``chunk_bwd``.
     Returns a dict: dq, dk (of the raw q, k; their dtype), dw_q, dw_k (fp32 or
-    None), dv, dg, dbeta, d_initial_state (fp32)."""
+    None), dv, dg, dbeta, d_initial_state (fp32). Repeated calls give the same
+    bits, but for dg and dbeta of the chunkwise path: they agree to rounding."""
     dev = ckpt.q.codes.get_device()
     if dev < 0 or stream is not None or dev != torch.cuda.current_device():
         with _on("chunk_bwd_packed", dev, stream, ckpt[:3], g, beta, d_o, initial_state, cu_seqlens,

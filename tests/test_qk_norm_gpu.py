@@ -638,3 +638,54 @@ def test_broadcast_gradients_are_refused():
             gdn.qk_norm_rope_bwd(dy, None, q, None)
     with pytest.raises(ValueError):
         gdn.qk_norm_rope_bwd(torch.ones((), device="cuda").expand(6, 2, 64), None, q, None)
+
+
+def test_rows_of_one_tensor_and_codes_of_the_other():
+    """pack=True with an output for q or k alone: the codes of both, the rows of one."""
+    import gated_delta_rule_112_b200 as gdn
+    q, k, w, how = make(19, 5, 3, 96, BF, 48, "rms", True, seed=68)
+    kw = dev(how, w)
+    ref = gdn.qk_norm_rope_fwd(q.cuda(), k.cuda(), pack=True, **kw)
+    for i in range(2):
+        out = [None, None]
+        out[i] = torch.empty_like((q, k)[i], device="cuda")
+        y = gdn.qk_norm_rope_fwd(q.cuda(), k.cuda(), pack=True, out=tuple(out), **kw)
+        assert torch.equal(y[i], ref[i]) and y[1 - i] is None
+        for a, b in zip(y[2:], ref[2:]):
+            assert torch.equal(a.codes.view(torch.uint8), b.codes.view(torch.uint8))
+            assert torch.equal(a.scales, b.scales)
+        with pytest.raises(gdn.GdnError):
+            gdn.qk_norm_rope_fwd(q.cuda(), k.cuda(), out=tuple(out), **kw)
+
+
+def test_training_step_captured_and_on_another_stream():
+    """Bit for bit, but for dg and dbeta: the chunkwise backward adds some 20 shares of each token's by atomics in
+    any order, which moves their sum by up to 20 units of 2^-24 of the shares (1.2e-6; summed over a chunk's
+    tokens for dg, the same of all shares). TOL_F32 leaves a factor of 8 for shares that cancel."""
+    import gated_delta_rule_112_b200 as gdn
+    gen = torch.Generator().manual_seed(92)
+    q, k, v, d_o = (torch.randn(2, 130, 2, 128, generator=gen).to(BF).cuda() for _ in range(4))
+    g = -torch.rand(2, 130, 2, generator=gen).cuda()
+    beta = torch.rand(2, 130, 2, generator=gen).cuda()
+
+    def step(**how):
+        o, fs, ck = gdn.chunk_fwd_packed(q, k, v, g, beta, **how)
+        return dict(gdn.chunk_bwd_packed(ck, g, beta, d_o, **how), o=o, fs=fs)
+
+    ref = {n: x.clone() for n, x in step().items() if x is not None}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = step(stream=side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for n in ref:
+        for out in (other, captured):
+            if n in ("dg", "dbeta"):
+                assert_close(n, np64(out[n]), np64(ref[n]), TOL_F32)
+            else:
+                assert torch.equal(ref[n], out[n]), n

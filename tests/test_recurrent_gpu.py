@@ -536,3 +536,68 @@ def test_calls_repeat_bit_for_bit():
         first = call(d, cu=cu)
         for _ in range(3):
             assert all(torch.equal(a, b) for a, b in zip(call(d, cu=cu), first))
+
+
+def test_slots_without_boundaries_and_boundaries_without_slots():
+    import gated_delta_rule_112_b200 as gdn
+    d = make([5] * 4, 2, 4, 128, 128, BF, seed=220, spare=0)         # equal runs: reset, keep and slots
+    how = dict(keep=[5, 2, 0, 4], reset=[True, False, True, False])
+    o, pool = call(d, cu=False, **how)
+    check(d, o, pool, **how)
+    d = make([3, 0, 6], 1, 2, 64, 32, F, BF, seed=221, spare=2)
+    pool = d["pool"].cuda()
+    o = gdn.recurrent_fwd(*(d[x].cuda() for x in ("q", "k", "v", "g", "beta")), pool, cu_seqlens=d["cu"].cuda())
+    d["slots"] = torch.arange(3, dtype=torch.int32)
+    check(d, o, pool)
+
+
+def test_no_runs_and_no_tokens():
+    import gated_delta_rule_112_b200 as gdn
+    d = make([2, 1], 1, 2, 128, 128, BF, seed=222)
+    args = [d[x].cuda() for x in ("q", "k", "v", "g", "beta")]
+    pool, out = d["pool"].cuda(), torch.full(tuple(d["v"].shape), 7.0, dtype=BF, device="cuda")
+    gdn.recurrent_fwd(*args, pool, ints([]), ints([0]), out=out)     # no runs: nothing is touched
+    assert bool((out == 7).all()) and torch.equal(pool.cpu(), d["pool"])
+    o = gdn.recurrent_fwd(*(x[:0] for x in args), pool, ints([2, 0]), ints([0, 0, 0]))
+    assert o.shape == (0, 2, 128) and torch.equal(pool.cpu(), d["pool"])
+
+
+@pytest.mark.parametrize("lens", [[6, 11], [1] * 5])
+def test_gates_off_their_alignment(lens):
+    """A channel gate that starts 4 bytes off a 16-byte boundary: read one by one."""
+    import gated_delta_rule_112_b200 as gdn
+    d = make(lens, 2, 4, 128, 128, BF, channel=True, seed=223)
+    wide = torch.zeros(d["g"].numel() + 1, device="cuda")
+    g = wide[1:].view(d["g"].shape)
+    g.copy_(d["g"])
+    pool = d["pool"].cuda()
+    o = gdn.recurrent_fwd(*(d[x].cuda() for x in "qkv"), g, d["beta"].cuda(), pool, d["slots"].cuda(),
+                          None if len(lens) == 5 else d["cu"].cuda())
+    check(d, o, pool)
+
+
+def test_a_captured_step_replayed_with_other_slots():
+    """A server's graph: one token a run, slots, keep and reset changed between replays."""
+    import gated_delta_rule_112_b200 as gdn
+    d = make([1] * 6, 2, 4, 128, 128, BF, seed=224, spare=6)
+    args = [d[x].cuda() for x in ("q", "k", "v", "g", "beta")]
+    pool, slots = d["pool"].cuda(), d["slots"].cuda()
+    keep, reset = ints([1] * 6), torch.zeros(6, dtype=torch.bool, device="cuda")
+    gdn.recurrent_fwd(*args, pool, slots, keep=keep, reset=reset)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = gdn.recurrent_fwd(*args, pool, slots, keep=keep, reset=reset)
+    for new, k, r in (([11, 0, 3, 7, 5, 2], [1, 0, 1, 1, 1, 0], [0, 0, 1, 0, 1, 1]),
+                      ([1, 2, -1, 4, 6, -4], [1, 1, 1, 0, 1, 1], [1, 0, 0, 0, 0, 1])):
+        pool.copy_(d["pool"])
+        out.fill_(7.0)
+        slots.copy_(ints(new))
+        keep.copy_(ints(k))
+        reset.copy_(ints(r).bool())
+        graph.replay()
+        torch.cuda.synchronize()
+        ro, rp = reference(d, keep=k, reset=r, slots=new)
+        on = [i for i in range(6) if new[i] >= 0]
+        assert_close("o", np64(out[on]), ro[on], tol(BF))
+        assert_close("pool", np64(pool), rp, TOL_F32)
+        assert all(bool((out[i] == 7).all()) for i in range(6) if new[i] < 0)
