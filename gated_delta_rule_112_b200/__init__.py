@@ -380,9 +380,10 @@ def recurrent_fwd(q, k, v, g, beta, pool, slots=None, cu_seqlens=None, keep=None
 
     Run n has tokens cu_seqlens[n] to cu_seqlens[n+1] (int32 [N+1]; without it
     all N runs have T/N) and its state in slot slots[n] (int32 [N]; without it
-    slot n; negative: padding, whose boundaries are not looked at). The state kept is that after its first keep[n]
-    tokens (int32 [N]; without it all; 0 leaves the slot alone); reset[n] (bool
-    [N]) starts it from zero. Tokens of no run keep what ``out`` held.
+    slot n; negative: padding, whose boundaries are not looked at). The state
+    kept is that after its first keep[n] tokens (int32 [N]; without it all; 0
+    leaves the slot alone); reset[n] (bool [N]) starts it from zero. Tokens of no
+    run keep what ``out`` held; ``out`` may not overlap an input.
     A run the device finds wrong (see gdn.h) leaves its state alone and has NaN
     outputs; ``status`` (see ``status_block``) then tells get_status."""
     name = "gdn_recurrent_fwd"

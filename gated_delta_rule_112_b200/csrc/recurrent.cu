@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kRecWarps * 32, 4) gdn_recurrent_kernel(const 
   const int kept = A.keep ? A.keep[n] : -2;
   const bool fresh = A.reset && A.reset[n];
   const bool outside = t0 < 0 || t1 < t0 || t1 > A.T;
-  const int len = t1 - t0;
+  const int len = int(unsigned(t1) - unsigned(t0));
   if (outside || slot < 0 || len == 0) {
     if (outside && slot >= 0 && tid == 0 && A.status) atomicOr(A.status, kErrBadSeqlens);
     return;
